@@ -434,14 +434,16 @@ permute_gather_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ i
             continue;
         }
         // pairs of this expert earlier in the chunk: any slot of an earlier
-        // token (token order), or the same slot of an earlier token (slot
-        // priority, where the chunk's base already counts earlier slots)
+        // token and earlier slots of the same one (token order; an expert may
+        // be named twice by a token), or the same slot of an earlier token
+        // (slot priority, where the chunk's base already counts earlier slots)
         int before = 0;
         if (kk > 1) {
             for (int q2 = 0; q2 < q; ++q2) before += (sidx[q2][j] == e);
         } else {
             for (int q2 = 0; q2 < q; ++q2)
                 for (int j2 = 0; j2 < k; ++j2) before += (sidx[q2][j2] == e);
+            for (int j2 = 0; j2 < j; ++j2) before += (sidx[q][j2] == e);
         }
         const int rank = blockoff[((size_t)e * kk + (kk > 1 ? j : 0)) * NB + chunk] + before;
         int p = -1;
