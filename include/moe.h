@@ -315,6 +315,98 @@ int moe_backward(const moe_problem* p, const void* x, const void* W_r, const voi
  * in place on the stream. */
 int moe_bias_update(const moe_problem* p, const void* stats, float gamma, float* bias, void* stream);
 
+/* ---- experts in 8-bit integers --------------------------------------------
+ * Beside moe_permute and moe_expert_up / moe_expert_down: the same layer with
+ * signed 8-bit activations and weights, a scale for each token and for each
+ * weight row (channel), and exact 32-bit integer sums. A forward in 8 bits is
+ *   moe_route, moe_permute_int8, moe_expert_up_int8, moe_quantize_rows (the
+ *   hidden rows), moe_expert_down_int8, moe_combine.
+ * p->dtype (bf16 or f32) is the type of x, h and o. d and d_ff are multiples
+ * of 16 (bf16: 64, as everywhere), at most 131071 each (the sums stay below
+ * 2^31), and d_ff_shared is 0: a shared expert is a second product with
+ * E = k = 1 over moe_quantize_rows(x), indptr = {0, T}. Otherwise
+ * MOE_ERR_UNSUPPORTED. Scales must be finite. Two calls that may overlap on
+ * the GPU need a workspace each. */
+
+/* Rows in 8 bits, also for the weights (one call over the rows of a matrix):
+ *   a_r = max_c |x[r,c]|, scale[r] = a_r / 127 (fp32),
+ *   q[r,c] = the whole number nearest to 127 x[r,c] / a_r, ties to even,
+ * decided exactly, so q depends on x alone. A row with a_r < 2^-100 gives
+ * zeros and scale 0. x [rows, cols] of dtype MOE_DTYPE_*, q [rows, cols],
+ * scale [rows]; cols % 16 == 0 (else MOE_ERR_UNSUPPORTED).
+ * used: NULL, or one device integer: only the first min(rows, *used) rows are
+ * read and written, the others stay as they are (pass &indptr[E] for the
+ * hidden rows of a layer). */
+int moe_quantize_rows(int32_t dtype, const void* x, int32_t rows, int32_t cols, const int32_t* used,
+                      int8_t* q, float* scale, void* stream);
+
+/* Bytes of workspace for the entry points below (256-byte aligned, no
+ * initialisation), 0 when p is not one they take. */
+size_t moe_int8_workspace_size(const moe_problem* p);
+
+/* moe_permute with the rows in 8 bits: pos, indptr, row_token and stats as
+ * there (row_token is required); xq [Rmax, d] and xs [Rmax] hold the
+ * quantised row of the token of each permuted row (each token is quantised
+ * once); padding rows get zeros and scale 0, rows >= indptr[E] stay. */
+int moe_permute_int8(const moe_problem* p, const void* x, const int32_t* idx,
+                     int32_t* pos, int32_t* indptr, int32_t* row_token, int8_t* xq, float* xs, void* stats,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Products over the permuted rows, with S(A, B)[r,n] = sum_c A[r,c] B_e[n,c]
+ * for a row r of expert e:
+ *   up:   a = S(xq, W1) xs[r] w1s[e,n], b = S(xq, W3) xs[r] w3s[e,n],
+ *         h[r,n] = SiLU(a) b
+ *   down: o[r,n] = S(hq, W2) hs[r] w2s[e,n]
+ * W1, W3 [E, d_ff, d], W2 [E, d, d_ff] int8; w1s, w3s [E, d_ff], w2s [E, d]
+ * fp32; h [Rmax, d_ff], o [Rmax, d] dtype, rows >= indptr[E] stay. indptr as
+ * in moe_experts. stats (may be NULL): only the status word is written. */
+int moe_expert_up_int8(const moe_problem* p, const int8_t* xq, const float* xs, const int32_t* indptr,
+                       const int8_t* W1, const float* w1s, const int8_t* W3, const float* w3s,
+                       void* h, void* stats, void* workspace, size_t workspace_bytes, void* stream);
+int moe_expert_down_int8(const moe_problem* p, const int8_t* hq, const float* hs, const int32_t* indptr,
+                         const int8_t* W2, const float* w2s,
+                         void* o, void* stats, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- the way back, with dropout, residual and gradients --------------------
+ * For training with experts of the caller's own, or through the stage entry
+ * points: moe_permute goes there, these come back. No train flag, no limit on
+ * E beyond MOE_MAX_E, bf16 and f32. Sums are fp32 in slot order, rounded once;
+ * repeated calls give identical bits; no workspace.
+ *
+ *   moe_combine_dropout: m_t = sum_{j kept} gate[t,j] o[pos[t,j]] (+ s[t]),
+ *                        out_t = residual_t + D(m_t)
+ *   moe_combine_backward, given dy = dL/dout, with u = D(dy):
+ *                        dO[pos[t,j]] = gate[t,j] u_t, dgate[t,j] = <u_t, o[pos[t,j]]>
+ *                        (0 for a dropped pair), ds_t = u_t
+ *                        (the residual's gradient is dy itself)
+ *   moe_permute_backward: dx_t = sum_{j kept} dxp[pos[t,j]]
+ *
+ * D is dropout with probability prob, in steps of 2^-16 (thr = round(65536
+ * prob), 0 <= prob, thr <= 65535); its mask is a function of the position
+ * and is never stored: element (t, c), i = t d + c, is kept when the 16-bit
+ * half i % 8 of Philox4x32-10(counter {i / 8, offset}, key seed) is at least
+ * thr (halves: word 0 low, word 0 high, word 1 low, ...), and kept values are
+ * scaled by 65536 / (65536 - thr). rng: two device uint64 {seed, offset}
+ * (8-byte aligned), read when the kernels run, so a captured graph draws
+ * anew when the program changes them between replays; the backward call gets
+ * the values of its forward. With thr == 0 rng is not read and may be NULL.
+ * Pass another offset for every layer and step.
+ *
+ *   o, dO, dxp [Rmax, d], pos [T, k], gate, dgate [T, k] fp32, s, residual,
+ *   out, dy, ds, dx [T, d]; s, residual and ds may be NULL. out may be the
+ *   residual, and dx or out may not overlap anything else that is read.
+ *   dO's rows of no pair stay as they are, except the padding rows of a
+ *   problem with pad_rows > 0, which become zeros: indptr [E+1] and row_token
+ *   [Rmax] of the permutation are required then (ignored otherwise).
+ *   A position outside [0, Rmax) counts as dropped. */
+int moe_combine_dropout(const moe_problem* p, const void* o, const int32_t* pos, const float* gate,
+                        const void* s, const void* residual, float prob, const uint64_t* rng,
+                        void* out, void* stream);
+int moe_combine_backward(const moe_problem* p, const void* dy, const void* o, const int32_t* pos, const float* gate,
+                         float prob, const uint64_t* rng, const int32_t* indptr, const int32_t* row_token,
+                         void* dO, float* dgate, void* ds, void* stream);
+int moe_permute_backward(const moe_problem* p, const void* dxp, const int32_t* pos, void* dx, void* stream);
+
 /* Human-readable text of an MOE_* code (static storage). */
 const char* moe_error_string(int code);
 

@@ -112,6 +112,23 @@ def _load():
     lib.moe_expert_down.restype = ctypes.c_int
     lib.moe_combine.argtypes = [P, vp, vp, vp, vp, vp, vp]
     lib.moe_combine.restype = ctypes.c_int
+    i32 = ctypes.c_int32
+    lib.moe_quantize_rows.argtypes = [i32, vp, i32, i32, vp, vp, vp, vp]
+    lib.moe_quantize_rows.restype = ctypes.c_int
+    lib.moe_int8_workspace_size.argtypes = [P]
+    lib.moe_int8_workspace_size.restype = sz
+    lib.moe_permute_int8.argtypes = [P] + [vp] * 8 + [vp, sz, vp]
+    lib.moe_permute_int8.restype = ctypes.c_int
+    lib.moe_expert_up_int8.argtypes = [P] + [vp] * 9 + [vp, sz, vp]
+    lib.moe_expert_up_int8.restype = ctypes.c_int
+    lib.moe_expert_down_int8.argtypes = [P] + [vp] * 7 + [vp, sz, vp]
+    lib.moe_expert_down_int8.restype = ctypes.c_int
+    lib.moe_combine_dropout.argtypes = [P] + [vp] * 5 + [f32, vp, vp, vp]
+    lib.moe_combine_dropout.restype = ctypes.c_int
+    lib.moe_combine_backward.argtypes = [P] + [vp] * 4 + [f32] + [vp] * 7
+    lib.moe_combine_backward.restype = ctypes.c_int
+    lib.moe_permute_backward.argtypes = [P] + [vp] * 4
+    lib.moe_permute_backward.restype = ctypes.c_int
     return lib
 
 
@@ -344,6 +361,113 @@ def permute_noalloc(p: Problem, x, idx, pos, indptr, row_token, xp, stats, strea
     rc = fn(ctypes.byref(p), _ptr(x), _ptr(idx), _ptr(pos), _ptr(indptr), _ptr(row_token), _ptr(xp), _ptr(stats),
             _stream(stream))
     _check(rc, "moe_permute_noalloc")
+
+
+# ---- experts in 8-bit integers ------------------------------------------------
+
+def int8_workspace_size(p: Problem) -> int:
+    n = int(_lib().moe_int8_workspace_size(ctypes.byref(p)))
+    if n == 0:
+        raise MoEError(MOE_ERR_UNSUPPORTED, "moe_int8_workspace_size")
+    return n
+
+
+def alloc_int8_workspace(p: Problem, device=None) -> torch.Tensor:
+    return torch.empty(int8_workspace_size(p), dtype=torch.uint8, device=device or "cuda")
+
+
+def quantize_rows(x, q=None, scale=None, used=None, stream=None):
+    """Rows of x [..., cols] in 8 bits with a scale for each row (see
+    moe_quantize_rows); used: a one-element int32 tensor, the rows to take.
+    Returns (q, scale), allocated here when not given."""
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _typed(q, torch.int8, rows * cols, "q")
+    _typed(scale, torch.float32, rows, "scale")
+    if used is not None:
+        _typed(used, torch.int32, 1, "used")
+    rc = _lib().moe_quantize_rows(_dtype_code(x.dtype), _ptr(x), rows, cols, _ptr(used), _ptr(q), _ptr(scale),
+                                  _stream(stream))
+    _check(rc, "moe_quantize_rows")
+    return q, scale
+
+
+def permute_int8(p: Problem, x, idx, pos, indptr, row_token, xq, xs, stats, workspace, stream=None):
+    """moe_permute with the token rows in 8 bits (see moe_permute_int8)."""
+    _typed(xq, torch.int8, permuted_rows(p) * p.d, "xq")
+    _typed(xs, torch.float32, permuted_rows(p), "xs")
+    rc = _lib().moe_permute_int8(ctypes.byref(p), _ptr(x), _ptr(idx), _ptr(pos), _ptr(indptr), _ptr(row_token),
+                                 _ptr(xq), _ptr(xs), _ptr(stats), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "moe_permute_int8")
+
+
+def expert_up_int8(p: Problem, xq, xs, indptr, W1, w1s, W3, w3s, h, workspace, stats=None, stream=None):
+    """h = SiLU(a) b over 8-bit rows and weights with their scales; see moe_expert_up_int8."""
+    _typed(xq, torch.int8, permuted_rows(p) * p.d, "xq")
+    _typed(W1, torch.int8, p.E * p.d_ff * p.d, "W1")
+    _typed(W3, torch.int8, p.E * p.d_ff * p.d, "W3")
+    rc = _lib().moe_expert_up_int8(ctypes.byref(p), _ptr(xq), _ptr(xs), _ptr(indptr), _ptr(W1), _ptr(w1s), _ptr(W3),
+                                   _ptr(w3s), _ptr(h), _ptr(stats), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "moe_expert_up_int8")
+
+
+def expert_down_int8(p: Problem, hq, hs, indptr, W2, w2s, o, workspace, stats=None, stream=None):
+    """o = hq W2^T over 8-bit rows and weights with their scales; see moe_expert_down_int8."""
+    _typed(hq, torch.int8, permuted_rows(p) * p.d_ff, "hq")
+    _typed(W2, torch.int8, p.E * p.d * p.d_ff, "W2")
+    rc = _lib().moe_expert_down_int8(ctypes.byref(p), _ptr(hq), _ptr(hs), _ptr(indptr), _ptr(W2), _ptr(w2s), _ptr(o),
+                                     _ptr(stats), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                     _stream(stream))
+    _check(rc, "moe_expert_down_int8")
+
+
+def _typed(t, dtype, numel, name):
+    """A tensor of another type or too small would be read as something else, or past its end."""
+    if t.dtype != dtype or t.numel() < numel:
+        raise ValueError(f"{name}: expected {dtype} with at least {numel} elements, got {t.dtype} with {t.numel()}")
+
+
+# ---- the way back, with dropout, residual and gradients -------------------------
+
+def combine_dropout(p: Problem, o, pos, gate, out, s=None, residual=None, prob=0.0, rng=None, stream=None):
+    """out_t = residual_t + dropout(sum_j gate[t,j] o[pos[t,j]] (+ s_t)); rng: a
+    device tensor of two 64-bit integers (seed, offset). See moe_combine_dropout."""
+    if rng is not None:
+        _rng(rng)
+    rc = _lib().moe_combine_dropout(ctypes.byref(p), _ptr(o), _ptr(pos), _ptr(gate), _ptr(s), _ptr(residual),
+                                    float(prob), _ptr(rng), _ptr(out), _stream(stream))
+    _check(rc, "moe_combine_dropout")
+    return out
+
+
+def combine_backward(p: Problem, dy, o, pos, gate, dO, dgate, ds=None, prob=0.0, rng=None, indptr=None,
+                     row_token=None, stream=None):
+    """Gradients of combine_dropout with the same prob and rng values:
+    dO[pos] = gate u, dgate = <u, o[pos]>, ds = u with u = dropout(dy); indptr
+    and row_token are needed with p.pad_rows > 0. See moe_combine_backward."""
+    if rng is not None:
+        _rng(rng)
+    rc = _lib().moe_combine_backward(ctypes.byref(p), _ptr(dy), _ptr(o), _ptr(pos), _ptr(gate), float(prob), _ptr(rng),
+                                     _ptr(indptr), _ptr(row_token), _ptr(dO), _ptr(dgate), _ptr(ds), _stream(stream))
+    _check(rc, "moe_combine_backward")
+
+
+def permute_backward(p: Problem, dxp, pos, dx, stream=None):
+    """dx_t = sum_j dxp[pos[t,j]] over the kept pairs; see moe_permute_backward."""
+    _check(_lib().moe_permute_backward(ctypes.byref(p), _ptr(dxp), _ptr(pos), _ptr(dx), _stream(stream)),
+           "moe_permute_backward")
+    return dx
+
+
+def _rng(rng):
+    if rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2:
+        raise ValueError("rng: expected two 64-bit integers (seed, offset)")
 
 
 @dataclass

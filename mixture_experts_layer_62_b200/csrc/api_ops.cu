@@ -1,0 +1,217 @@
+// C ABI of the operators beside the layer: argument checks, the workspace of
+// the 8-bit experts and the launch sequences. Every launch is asynchronous on
+// the caller's stream; the host never waits on the device.
+#include <cmath>
+
+#include "ops.cuh"
+
+namespace moe {
+
+I8Layout make_i8_layout(const moe_problem& p) {
+    const size_t T = p.T > 0 ? (size_t)p.T : 0, E = (size_t)p.E;
+    const size_t NB = (T + kChunk - 1) / kChunk, kk = (size_t)count_slots(p);
+    I8Layout L;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        size_t o = off;
+        off = align_up(off + (bytes > 0 ? bytes : 1), 256);
+        return o;
+    };
+    L.blockcnt = take(E * kk * NB * 4);
+    L.blockoff = take(E * kk * NB * 4);
+    L.tiles = take((E + 2) * 4);
+    L.status = take(4);
+    L.total = off;
+    return L;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+namespace {
+
+constexpr int kMaxI8K = 131071;   // K 128^2 stays below 2^31
+
+#define CK(expr)                                   \
+    do {                                           \
+        if ((expr) != cudaSuccess) return MOE_ERR_CUDA; \
+    } while (0)
+
+bool ok16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool ok4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// optional pointers: absent, or aligned
+bool opt16(const void* p) { return p == nullptr || ok16(p); }
+
+int check_int8(const moe_problem* p) {
+    const int rc = check_problem(p);
+    if (rc != MOE_OK) return rc;
+    if (p->d % 16 || p->d_ff % 16 || p->d_ff_shared || p->d > kMaxI8K || p->d_ff > kMaxI8K) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// 0: dropout of probability prob from rng; MOE_ERR_* otherwise
+int make_dropout(float prob, const uint64_t* rng, Dropout* d) {
+    if (!(prob >= 0.f) || !(prob < 1.f)) return MOE_ERR_INVALID_ARG;
+    const long thr = std::lround((double)prob * 65536.0);
+    if (thr > 65535) return MOE_ERR_INVALID_ARG;
+    d->rng = nullptr;
+    d->thr = (unsigned)thr;
+    d->scale = (float)(65536.0 / (65536.0 - (double)thr));
+    if (thr == 0) return MOE_OK;
+    if (rng == nullptr || (reinterpret_cast<uintptr_t>(rng) & 7u)) return MOE_ERR_INVALID_ARG;
+    d->rng = reinterpret_cast<const unsigned long long*>(rng);
+    return MOE_OK;
+}
+
+int i8_workspace(const moe_problem* p, void* ws, size_t bytes, I8Layout* L) {
+    *L = make_i8_layout(*p);
+    if (!ws || bytes < L->total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_WORKSPACE;
+    return MOE_OK;
+}
+
+int run_i8(const moe_problem* p, const int8_t* A, const float* sa, const int32_t* indptr, const int8_t* B0,
+           const float* sb0, const int8_t* B1, const float* sb1, void* out, int N, int K, void* stats, void* workspace,
+           const I8Layout& L, void* stream) {
+    char* ws = static_cast<char*>(workspace);
+    I8Gemm g = {};
+    g.indptr = indptr; g.E = p->E;
+    g.A = A; g.sa = sa; g.B0 = B0; g.sb0 = sb0; g.B1 = B1; g.sb1 = sb1;
+    g.out = out; g.out_dtype = p->dtype; g.N = N; g.K = K; g.rows = (int)permuted_rows(*p);
+    g.status = stats ? static_cast<int32_t*>(stats) : reinterpret_cast<int32_t*>(ws + L.status);
+    g.tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
+    CK(launch_i8_gemm(g, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_int8_workspace_size(const moe_problem* p) {
+    if (check_int8(p) != MOE_OK) return 0;
+    return make_i8_layout(*p).total;
+}
+
+int moe_quantize_rows(int32_t dtype, const void* x, int32_t rows, int32_t cols, const int32_t* used, int8_t* q,
+                      float* scale, void* stream) {
+    if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+    if (rows < 0 || cols <= 0) return MOE_ERR_INVALID_ARG;
+    if (cols % 16) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MOE_OK;
+    if (!ok16(x) || !ok16(q) || !ok4(scale) || (used != nullptr && !ok4(used))) return MOE_ERR_INVALID_ARG;
+    CK(launch_quantize_rows(dtype, x, rows, cols, used, q, scale, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_permute_int8(const moe_problem* p, const void* x, const int32_t* idx, int32_t* pos, int32_t* indptr,
+                     int32_t* row_token, int8_t* xq, float* xs, void* stats, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+    int rc = check_int8(p);
+    if (rc != MOE_OK) return rc;
+    if (!ok4(idx) || !ok4(pos) || !ok4(indptr) || !ok4(row_token) || !ok16(stats) || !ok4(xs)) return MOE_ERR_INVALID_ARG;
+    if (!ok16(x) || !ok16(xq)) return MOE_ERR_INVALID_ARG;
+    I8Layout L;
+    rc = i8_workspace(p, workspace, workspace_bytes, &L);
+    if (rc != MOE_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int C = capacity_of(p);
+    if (p->T == 0) {
+        CK(launch_zero_stats(stats, p->E, C, st));
+        CK(cudaMemsetAsync(indptr, 0, sizeof(int32_t) * (size_t)(p->E + 1), st));
+        return MOE_OK;
+    }
+    char* ws = static_cast<char*>(workspace);
+    int32_t* blockcnt = reinterpret_cast<int32_t*>(ws + L.blockcnt);
+    int32_t* blockoff = reinterpret_cast<int32_t*>(ws + L.blockoff);
+    const int kk = count_slots(*p);
+    CK(launch_hist(idx, p->T, p->k, kk, p->E, blockcnt, st));
+    ScanArgs sa = {};
+    sa.T = p->T; sa.k = p->k; sa.E = p->E; sa.capacity = C; sa.kk = kk;
+    sa.blockcnt = blockcnt; sa.blockoff = blockoff;
+    sa.indptr = indptr; sa.stats = stats;
+    sa.pad = p->pad_rows;
+    CK(launch_scan(sa, st));
+    CK(launch_permute_gather(p->dtype, nullptr, idx, blockoff, indptr, p->T, p->d, p->E, p->k, kk, C, pos, row_token,
+                             nullptr, st));
+    CK(launch_quantize_scatter(p->dtype, x, pos, p->T, p->d, p->k, (int)permuted_rows(*p), xq, xs, st));
+    if (p->pad_rows > 0) CK(launch_pad_rows_i8(indptr, stats, p->E, p->d, xq, xs, row_token, p->pad_rows, st));
+    return MOE_OK;
+}
+
+int moe_expert_up_int8(const moe_problem* p, const int8_t* xq, const float* xs, const int32_t* indptr,
+                       const int8_t* W1, const float* w1s, const int8_t* W3, const float* w3s, void* h, void* stats,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_int8(p);
+    if (rc != MOE_OK) return rc;
+    if (!ok16(xq) || !ok16(W1) || !ok16(W3) || !ok16(h) || !ok4(xs) || !ok16(w1s) || !ok16(w3s) || !ok4(indptr) || !opt16(stats))
+        return MOE_ERR_INVALID_ARG;
+    I8Layout L;
+    rc = i8_workspace(p, workspace, workspace_bytes, &L);
+    if (rc != MOE_OK) return rc;
+    if (p->T == 0) return MOE_OK;
+    return run_i8(p, xq, xs, indptr, W1, w1s, W3, w3s, h, p->d_ff, p->d, stats, workspace, L, stream);
+}
+
+int moe_expert_down_int8(const moe_problem* p, const int8_t* hq, const float* hs, const int32_t* indptr,
+                         const int8_t* W2, const float* w2s, void* o, void* stats, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    int rc = check_int8(p);
+    if (rc != MOE_OK) return rc;
+    if (!ok16(hq) || !ok16(W2) || !ok16(o) || !ok4(hs) || !ok16(w2s) || !ok4(indptr) || !opt16(stats))
+        return MOE_ERR_INVALID_ARG;
+    I8Layout L;
+    rc = i8_workspace(p, workspace, workspace_bytes, &L);
+    if (rc != MOE_OK) return rc;
+    if (p->T == 0) return MOE_OK;
+    return run_i8(p, hq, hs, indptr, W2, w2s, nullptr, nullptr, o, p->d, p->d_ff, stats, workspace, L, stream);
+}
+
+int moe_combine_dropout(const moe_problem* p, const void* o, const int32_t* pos, const float* gate, const void* s,
+                        const void* residual, float prob, const uint64_t* rng, void* out, void* stream) {
+    int rc = check_problem(p);
+    if (rc != MOE_OK) return rc;
+    MixArgs a = {};
+    rc = make_dropout(prob, rng, &a.drop);
+    if (rc != MOE_OK) return rc;
+    if (p->T == 0) return MOE_OK;
+    if (!ok16(o) || !ok4(pos) || !ok4(gate) || !ok16(out) || !opt16(s) || !opt16(residual)) return MOE_ERR_INVALID_ARG;
+    a.dtype = p->dtype; a.o = o; a.pos = pos; a.gate = gate; a.s = s; a.residual = residual; a.out = out;
+    a.T = p->T; a.d = p->d; a.k = p->k; a.rows = (int)permuted_rows(*p);
+    CK(launch_mix(a, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_combine_backward(const moe_problem* p, const void* dy, const void* o, const int32_t* pos, const float* gate,
+                         float prob, const uint64_t* rng, const int32_t* indptr, const int32_t* row_token, void* dO,
+                         float* dgate, void* ds, void* stream) {
+    int rc = check_problem(p);
+    if (rc != MOE_OK) return rc;
+    MixBackArgs a = {};
+    rc = make_dropout(prob, rng, &a.drop);
+    if (rc != MOE_OK) return rc;
+    if (p->T == 0) return MOE_OK;
+    if (!ok16(dy) || !ok16(o) || !ok4(pos) || !ok4(gate) || !ok16(dO) || !ok4(dgate) || !opt16(ds)) return MOE_ERR_INVALID_ARG;
+    if (p->pad_rows > 0) {
+        if (!ok4(indptr) || !ok4(row_token)) return MOE_ERR_INVALID_ARG;
+        a.indptr = indptr; a.row_token = row_token;
+    }
+    a.dtype = p->dtype; a.dy = dy; a.o = o; a.pos = pos; a.gate = gate; a.dO = dO; a.dgate = dgate; a.ds = ds;
+    a.T = p->T; a.d = p->d; a.k = p->k; a.rows = (int)permuted_rows(*p); a.E = p->E;
+    CK(launch_mix_back(a, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_permute_backward(const moe_problem* p, const void* dxp, const int32_t* pos, void* dx, void* stream) {
+    int rc = check_problem(p);
+    if (rc != MOE_OK) return rc;
+    if (p->T == 0) return MOE_OK;
+    if (!ok16(dxp) || !ok4(pos) || !ok16(dx)) return MOE_ERR_INVALID_ARG;
+    MixArgs a = {};
+    a.dtype = p->dtype; a.o = dxp; a.pos = pos; a.out = dx;
+    a.T = p->T; a.d = p->d; a.k = p->k; a.rows = (int)permuted_rows(*p);
+    CK(launch_mix(a, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+}  // extern "C"

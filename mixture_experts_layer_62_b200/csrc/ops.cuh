@@ -1,0 +1,87 @@
+// Declarations of the operators beside the layer: products in 8-bit integers
+// (quantisation, permutation, grouped products) and the way back with
+// dropout, residual and gradients.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// ---- 8-bit experts ----------------------------------------------------------
+
+// Byte offsets of moe_int8_workspace_size(p) bytes.
+struct I8Layout {
+    size_t blockcnt, blockoff;   // permutation: per-chunk expert counts and their scan
+    size_t tiles;                // cumulative tiles per group [E + 2]
+    size_t status;               // status word of a call without a statistics block
+    size_t total;
+};
+I8Layout make_i8_layout(const moe_problem& p);
+
+// One product of the experts: out[r][n] over the rows of every group.
+struct I8Gemm {
+    const int32_t* indptr;   // [E+1] (device)
+    int E;
+    const int8_t* A;         // [rows, K]
+    const float* sa;         // [rows]
+    const int8_t* B0;        // [E, N, K]
+    const float* sb0;        // [E, N]
+    const int8_t* B1;        // second weight of the SwiGLU form, or null
+    const float* sb1;
+    void* out;               // [rows, N] bf16 or fp32
+    int out_dtype;
+    int N, K, rows;
+    int32_t* status;
+    int32_t* tiles;          // workspace for the tile schedule [E + 2]
+};
+cudaError_t launch_i8_gemm(const I8Gemm& g, cudaStream_t st);
+
+// rows of x -> q, scale; only the first min(rows, *used) rows when used != null
+cudaError_t launch_quantize_rows(int dtype, const void* x, int rows, int cols, const int32_t* used, int8_t* q,
+                                 float* scale, cudaStream_t st);
+// the rows of x [T, d], each to its kept destinations pos[t, :]
+cudaError_t launch_quantize_scatter(int dtype, const void* x, const int32_t* pos, int T, int d, int k, int rows,
+                                    int8_t* xq, float* xs, cudaStream_t st);
+// zeros in the padding rows (row_token < 0) of [0, indptr[E])
+cudaError_t launch_pad_rows_i8(const int32_t* indptr, const void* stats, int E, int d, int8_t* xq, float* xs,
+                               int32_t* row_token, int pad, cudaStream_t st);
+
+// ---- the way back -----------------------------------------------------------
+
+// Dropout of [T, d] values: keep element i = t d + c when the 16-bit half
+// i % 8 of the generator's block i / 8 is at least thr; scale = 65536 / (65536 - thr).
+struct Dropout {
+    const unsigned long long* rng;   // {seed, offset} (device); null: no dropout
+    unsigned thr;
+    float scale;
+};
+struct MixArgs {
+    int dtype;
+    const void* o;           // [rows, d]
+    const int32_t* pos;      // [T, k]
+    const float* gate;       // [T, k], or null: every gate is 1
+    const void* s;           // [T, d] or null
+    const void* residual;    // [T, d] or null
+    void* out;               // [T, d]
+    int T, d, k, rows;
+    Dropout drop;
+};
+cudaError_t launch_mix(const MixArgs& a, cudaStream_t st);
+
+struct MixBackArgs {
+    int dtype;
+    const void* dy;          // [T, d]
+    const void* o;           // [rows, d]
+    const int32_t* pos;
+    const float* gate;
+    void* dO;                // [rows, d]
+    float* dgate;            // [T, k]
+    void* ds;                // [T, d] or null
+    const int32_t* indptr;   // padded layouts: [E+1] and row_token [rows], else null
+    const int32_t* row_token;
+    int T, d, k, rows, E;
+    Dropout drop;
+};
+cudaError_t launch_mix_back(const MixBackArgs& a, cudaStream_t st);
+
+}  // namespace moe

@@ -1,0 +1,266 @@
+"""8-bit experts on the GPU: quantisation, permutation and products against
+64-bit plain forms (tests/ops_ref.py)."""
+
+import math
+
+import pytest
+import torch
+
+import mixture_experts_layer_62_b200 as moe
+import ops_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape):
+    return torch.randn(shape, generator=g, device=DEV)
+
+
+def ints(g, *shape):
+    return torch.randint(-128, 128, shape, generator=g, device=DEV, dtype=torch.int8)
+
+
+# ---- quantisation -------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (3, 2048), (5, 2064), (7, 4096), (130, 8192), (9, 8208), (4, 14336),
+                                       (3, 16400), (2, 131072), (2000, 208)])
+def test_quantize_rows(rows, cols, dtype):
+    g = gen(rows * 7 + cols)
+    x = randn(g, rows, cols) * torch.exp(4 * randn(g, rows, 1))
+    x = x.to(DT[dtype])
+    q, s = moe.quantize_rows(x)
+    R.check_quantized(x, q, s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_quantize_rows_at_the_borders(dtype):
+    # whole rows of exact ties and of values one step of the type beside them:
+    # a = 127 2^e makes the steps whole, so x = m + 1/2 are ties
+    rows = []
+    for scale in (1.0, 2.0 ** -30, 2.0 ** 20):
+        ties = torch.tensor([127.0] + [m + 0.5 for m in range(-63, 63)] + [-127.0])
+        rows += [ties * scale]
+    # a = 1: 127 x is a tie at x = (m + 1/2) / 127, not representable; its two neighbours in the type
+    near = torch.tensor([(m + 0.5) / 127 for m in range(-63, 63)], dtype=torch.float64).to(DT[dtype]).float()
+    one = torch.ones(1)
+    rows += [torch.cat([one, near, -one])]
+    up = torch.nextafter(near, torch.full_like(near, 9.0)) if dtype == "f32" else near
+    rows += [torch.cat([one, up, -one])]
+    # maxima that are no powers of two
+    g = torch.Generator().manual_seed(3)
+    for _ in range(40):
+        a = torch.rand(1, generator=g) + 0.5
+        m = torch.randint(-127, 127, (126,), generator=g).double() + 0.5
+        rows += [torch.cat([a, (m * a.double() / 127).float().clamp(-a.item(), a.item()), -a])]
+    x = torch.stack([r.to(DT[dtype]) for r in rows]).to(DEV)
+    q, s = moe.quantize_rows(x)
+    R.check_quantized(x, q, s)
+
+
+def test_quantize_rows_tiny_zero_and_unused_rows():
+    x = torch.zeros((6, 48), device=DEV)
+    x[1, 3] = 2.0 ** -101          # below the floor: a row of zeros
+    x[2, 5] = 2.0 ** -100          # on it
+    x[3] = 3.0e38                  # the largest values
+    x[4:] = float("nan")           # rows that nobody uses may hold anything
+    q = torch.full((6, 48), 77, dtype=torch.int8, device=DEV)
+    s = torch.full((6,), 5.0, device=DEV)
+    moe.quantize_rows(x, q, s, used=torch.tensor([4], dtype=torch.int32, device=DEV))
+    R.check_quantized(x[:4], q[:4], s[:4])
+    assert q[1].abs().max() == 0 and s[1] == 0 and q[2, 5] == 127 and (q[3] == 127).all()
+    assert (q[4:] == 77).all() and (s[4:] == 5.0).all()
+    # used past the rows, and none used
+    moe.quantize_rows(x[:4], q, s, used=torch.tensor([900], dtype=torch.int32, device=DEV))
+    R.check_quantized(x[:4], q[:4], s[:4])
+    q.fill_(9)
+    moe.quantize_rows(x, q, s, used=torch.tensor([0], dtype=torch.int32, device=DEV))
+    assert (q == 9).all()
+
+
+# ---- permutation --------------------------------------------------------------
+
+PERM = [dict(T=1, E=8, k=2), dict(T=1, E=1, k=1), dict(T=3, E=5, k=5), dict(T=31, E=7, k=3, cf=0.8),
+        dict(T=200, E=8, k=2, cf=1.0, drop=1), dict(T=257, E=16, k=4, pad=64, skew=1.5),
+        dict(T=64, E=512, k=16, pad=128, cf=1.0), dict(T=900, E=9, k=8, pad=128, drop=1, cf=0.7),
+        dict(T=3000, E=64, k=8, cf=1.2, skew=1.0), dict(T=5000, E=3, k=1), dict(T=1025, E=4, k=2, drop=1, cf=0.5, pad=64)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", PERM, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
+def test_permute_int8(c, dtype):
+    T, E, k = c["T"], c["E"], c["k"]
+    d = 192 if dtype == "bf16" else 208
+    p = moe.problem(T, d, 64, E, k, c.get("cf", 0.0), dtype, drop_order=c.get("drop", 0), pad_rows=c.get("pad", 0))
+    g = gen(T + E)
+    x = (randn(g, T, d) * torch.exp(randn(g, T, 1))).to(DT[dtype])
+    idx = R.routed(T, E, k, T * 31 + E, c.get("skew", 0.0))
+    if T > 2:
+        idx[1] = idx[1, 0]          # the same expert in every slot of a token
+        idx[2, 0] = -1              # not an expert: the pair takes no row
+    idx = idx.to(DEV)
+    N = moe.permuted_rows(p)
+    pos = torch.full((T, k), -7, dtype=torch.int32, device=DEV)
+    indptr = torch.full((E + 1,), -7, dtype=torch.int32, device=DEV)
+    rt = torch.full((N,), -7, dtype=torch.int32, device=DEV)
+    xq = torch.full((N, d), 99, dtype=torch.int8, device=DEV)
+    xs = torch.full((N,), -3.0, device=DEV)
+    st, ws = moe.alloc_stats(E, DEV), moe.alloc_int8_workspace(p, DEV)
+    st.fill_(255)
+    ws.fill_(255)
+    moe.permute_int8(p, x, idx, pos, indptr, rt, xq, xs, st, ws)
+    cap = R.capacity(c.get("cf", 0.0), T, k, E)
+    pos_r, ind_r, rt_r, kept, count = R.permutation(idx, E, cap, c.get("pad", 0), bool(c.get("drop", 0)))
+    assert (pos.cpu().numpy() == pos_r).all()
+    assert (indptr.cpu().numpy() == ind_r).all()
+    n = int(ind_r[-1])
+    assert (rt[:n].cpu().numpy() == rt_r).all()
+    assert (rt[n:] == -7).all() and (xq[n:] == 99).all() and (xs[n:] == -3.0).all()
+    real = torch.from_numpy(rt_r).to(DEV)
+    on = real >= 0
+    R.check_quantized(x[real[on]], xq[:n][on], xs[:n][on])
+    assert (xq[:n][~on] == 0).all() and (xs[:n][~on] == 0).all()
+    s = moe.read_stats(st, E)
+    assert s.status == 0 and s.kept == kept.tolist() and s.counts == count.tolist()
+    assert s.rows == int(kept.sum()) and s.dropped == int((count - kept).sum()) and s.max_count == int(count.max())
+    assert s.capacity == (-1 if cap is None else cap)
+
+
+# ---- products -----------------------------------------------------------------
+
+def split(total, E, g):
+    """Random group ends with empty groups among them."""
+    cut = torch.randint(0, total + 1, (E - 1,), generator=torch.Generator().manual_seed(g)).sort().values
+    return torch.cat([torch.zeros(1, dtype=torch.long), cut, torch.tensor([total])]).to(torch.int32)
+
+
+def run_products(T, d, dff, E, k, dtype, indptr, g, ws_fill=255, stats=True, scale_a=None):
+    """Both products over given groups; results against the plain form."""
+    p = moe.problem(T, d, dff, E, k, 0.0, dtype)
+    N, dt = moe.permuted_rows(p), DT[dtype]
+    indptr = indptr.to(DEV)
+    n = int(indptr[-1])
+    ws = moe.alloc_int8_workspace(p, DEV)
+    ws.fill_(ws_fill)
+    st = moe.alloc_stats(E, DEV)
+    st.fill_(255)
+    xq, hq = ints(g, N, d), ints(g, N, dff)
+    # scales that give pre-activations around 1, and some far out
+    xs = torch.rand((N,), generator=g, device=DEV) * (4.0 / (74 * 74 * math.sqrt(d)))
+    xs[::5] *= 30
+    hs = torch.rand((N,), generator=g, device=DEV) / (74 * 74 * math.sqrt(dff))
+    W1, W3, W2 = ints(g, E, dff, d), ints(g, E, dff, d), ints(g, E, d, dff)
+    w1s, w3s, w2s = (0.5 + torch.rand((E, m), generator=g, device=DEV) for m in (dff, dff, d))
+    xs[n:] = float("nan")    # rows of no group: whatever they hold is not looked at
+    hs[n:] = float("nan")
+    h = torch.full((N, dff), 7.0, dtype=dt, device=DEV)
+    o = torch.full((N, d), 7.0, dtype=dt, device=DEV)
+    moe.expert_up_int8(p, xq, xs, indptr, W1, w1s, W3, w3s, h, ws, stats=st if stats else None)
+    if stats:
+        assert moe.read_stats(st, E).status == moe.MOE_OK
+        st.fill_(255)
+    moe.expert_down_int8(p, hq, hs, indptr, W2, w2s, o, ws, stats=st if stats else None)
+    if stats:
+        assert moe.read_stats(st, E).status == moe.MOE_OK
+    a, b = R.product(xq[:n], xs[:n], W1, w1s, indptr), R.product(xq[:n], xs[:n], W3, w3s, indptr)
+    ref = R.swiglu(a, b)
+    assert ((h[:n].double() - ref).abs() <= R.swiglu_bound(a, b, dt)).all()
+    ref = R.product(hq[:n], hs[:n], W2, w2s, indptr)
+    assert ((o[:n].double() - ref).abs() <= R.plain_bound(ref, dt)).all()
+    assert (h[n:] == 7.0).all() and (o[n:] == 7.0).all()
+    return h, o
+
+
+SMALL = [(1, 64, 64, 1, 1), (1, 128, 192, 8, 2), (4, 256, 448, 8, 2), (5, 1088, 320, 4, 2), (9, 64, 2048, 3, 3),
+         (16, 512, 512, 8, 2), (33, 192, 128, 2, 2), (40, 4096, 1024, 8, 2), (100, 256, 256, 16, 4),
+         (250, 320, 576, 8, 2), (300, 64, 64, 64, 8)]
+LARGE = [(1024, 512, 256, 4, 2), (2000, 192, 448, 8, 2), (700, 1024, 640, 1, 1), (3000, 256, 320, 5, 1),
+         (513, 2048, 1408, 2, 2)]
+
+
+@pytest.mark.parametrize("T,d,dff,E,k", SMALL + LARGE)
+def test_products_bf16(T, d, dff, E, k):
+    g = gen(T * 3 + d)
+    for s in range(2):
+        run_products(T, d, dff, E, k, "bf16", split(T * k, E, s + T), g, stats=s == 0)
+    if k == 1 or E > 1:
+        one = torch.zeros(E + 1, dtype=torch.int32)
+        one[E // 2 + 1:] = T * k    # every row in one group
+        run_products(T, d, dff, E, k, "bf16", one, g, ws_fill=0)
+
+
+@pytest.mark.parametrize("T,d,dff,E,k", [(1, 16, 16, 1, 1), (3, 48, 80, 2, 2), (77, 208, 336, 5, 3), (8, 1040, 272, 4, 1),
+                                         (600, 144, 176, 3, 2), (1500, 400, 240, 2, 2)])
+def test_products_f32(T, d, dff, E, k):
+    g = gen(T + dff)
+    run_products(T, d, dff, E, k, "f32", split(T * k, E, T), g)
+    if k == 1 or E > 1:
+        short = split(T * k, E, T + 1).clamp(max=T * k // 2)   # half of the rows in no group
+        run_products(T, d, dff, E, k, "f32", short, g)
+
+
+def test_products_without_rows():
+    g = gen(1)
+    for T in (1, 9, 600):
+        run_products(T, 128, 64, 4, 2, "bf16", torch.zeros(5, dtype=torch.int32), g)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 12, 140, 400])
+def test_products_at_the_largest_sums(rows):
+    # every product (-128)^2 over the longest K that is taken: the sums reach 2^31 - 2^14 or so
+    K, N = 131056, 16
+    p = moe.problem(rows, N, K, 1, 1, 0.0, "f32")
+    ws = moe.alloc_int8_workspace(p, DEV)
+    hq = torch.full((rows, K), -128, dtype=torch.int8, device=DEV)
+    W2 = torch.full((1, N, K), -128, dtype=torch.int8, device=DEV)
+    W2[0, 1] = 127
+    hs = torch.ones(rows, device=DEV)
+    o = torch.zeros((rows, N), device=DEV)
+    moe.expert_down_int8(p, hq, hs, torch.tensor([0, rows], dtype=torch.int32, device=DEV), W2,
+                         torch.ones((1, N), device=DEV), o, ws)
+    want = torch.full((rows, N), float(K) * 128 * 128, device=DEV)
+    want[:, 1] = -float(K) * 128 * 127
+    assert torch.equal(o, want.to(torch.float64).float())
+
+
+@pytest.mark.parametrize("T", [2, 60, 900])
+def test_products_are_the_same_bits_again(T):
+    a = run_products(T, 256, 320, 4, 2, "bf16", split(T * 2, 4, 5), gen(11))
+    b = run_products(T, 256, 320, 4, 2, "bf16", split(T * 2, 4, 5), gen(11), ws_fill=3)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_products_past_32_bit_offsets():
+    # W1 / W3 beyond 2^31 bytes, rows of the last expert among them; plain form on that expert alone
+    E, dff, d, T = 40, 8192, 8192, 3
+    p = moe.problem(T, d, dff, E, 1, 0.0, "bf16")
+    g = gen(2)
+    W = torch.zeros((E, dff, d), dtype=torch.int8, device=DEV)
+    W[E - 1] = ints(g, dff, d)
+    ws_ = torch.ones((E, dff), device=DEV)
+    xq, xs = ints(g, T, d), torch.full((T,), 1.0 / (74 * 74 * 90), device=DEV)
+    indptr = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    indptr[E] = T
+    h = torch.zeros((T, dff), dtype=torch.bfloat16, device=DEV)
+    moe.expert_up_int8(p, xq, xs, indptr, W, ws_, W, ws_, h, moe.alloc_int8_workspace(p, DEV))
+    a = R.product(xq, xs, W[E - 1:], ws_[:1], torch.tensor([0, T]))
+    assert ((h.double() - R.swiglu(a, a)).abs() <= R.swiglu_bound(a, a, torch.bfloat16)).all()
+
+
+# ---- the chain, streams and graphs ------------------------------------------------
+
+def layer_inputs(T, d, dff, E, k, seed, dfs=0):
+    g = gen(seed)
+    n = lambda *s: (randn(g, *s) / math.sqrt(s[-1])).to(torch.bfloat16)  # noqa: E731
+    w = dict(W_r=(randn(g, d, E) / math.sqrt(d)).to(torch.bfloat16), W1=n(E, dff, d), W3=n(E, dff, d), W2=n(E, d, dff))
+    if dfs:
+        w |= dict(Ws1=n(dfs, d), Ws3=n(dfs, d), Ws2=n(d, dfs))
+    return randn(g, T, d).to(torch.bfloat16), w
