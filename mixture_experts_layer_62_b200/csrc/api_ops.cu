@@ -19,10 +19,15 @@ I8Layout make_i8_layout(const moe_problem& p) {
     };
     L.blockcnt = take(E * kk * NB * 4);
     L.blockoff = take(E * kk * NB * 4);
-    L.tiles = take((E + 2) * 4);
     L.status = take(4);
     L.total = off;
     return L;
+}
+
+I8Form i8_form(const moe_problem& p) {
+    const long long rows = permuted_rows(p);
+    if (rows <= 16) return I8_STREAM;
+    return rows >= 256LL * p.E ? I8_PAIR : I8_SINGLE;
 }
 
 }  // namespace moe
@@ -79,8 +84,9 @@ int run_i8(const moe_problem* p, const int8_t* A, const float* sa, const int32_t
     g.A = A; g.sa = sa; g.B0 = B0; g.sb0 = sb0; g.B1 = B1; g.sb1 = sb1;
     g.out = out; g.out_dtype = p->dtype; g.N = N; g.K = K; g.rows = (int)permuted_rows(*p);
     g.status = stats ? static_cast<int32_t*>(stats) : reinterpret_cast<int32_t*>(ws + L.status);
-    g.tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
-    CK(launch_i8_gemm(g, static_cast<cudaStream_t>(stream)));
+    g.form = i8_form(*p);
+    CK(g.form == I8_STREAM ? launch_i8_gemm(g, static_cast<cudaStream_t>(stream))
+                           : launch_i8_tc(g, static_cast<cudaStream_t>(stream)));
     return MOE_OK;
 }
 

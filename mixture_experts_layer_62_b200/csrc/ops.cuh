@@ -12,14 +12,16 @@ namespace moe {
 // Byte offsets of moe_int8_workspace_size(p) bytes.
 struct I8Layout {
     size_t blockcnt, blockoff;   // permutation: per-chunk expert counts and their scan
-    size_t tiles;                // cumulative tiles per group [E + 2]
     size_t status;               // status word of a call without a statistics block
     size_t total;
 };
 I8Layout make_i8_layout(const moe_problem& p);
 
 // One product of the experts: out[r][n] over the rows of every group.
+enum I8Form { I8_STREAM = 0, I8_SINGLE = 1, I8_PAIR = 2 };
+I8Form i8_form(const moe_problem& p);
 struct I8Gemm {
+    int form;
     const int32_t* indptr;   // [E+1] (device)
     int E;
     const int8_t* A;         // [rows, K]
@@ -32,9 +34,9 @@ struct I8Gemm {
     int out_dtype;
     int N, K, rows;
     int32_t* status;
-    int32_t* tiles;          // workspace for the tile schedule [E + 2]
 };
 cudaError_t launch_i8_gemm(const I8Gemm& g, cudaStream_t st);
+cudaError_t launch_i8_tc(const I8Gemm& g, cudaStream_t st);
 
 // rows of x -> q, scale; only the first min(rows, *used) rows when used != null
 cudaError_t launch_quantize_rows(int dtype, const void* x, int rows, int cols, const int32_t* used, int8_t* q,
