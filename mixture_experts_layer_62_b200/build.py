@@ -31,7 +31,7 @@ DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libmoe_debug.so")
 
 SOURCES = ["api.cu", "route.cu", "permute.cu", "combine.cu", "gemm_simt.cu", "gemm_sm100.cu",
            "permute_noalloc.cu", "route_small.cu", "gemm_bwd_sm100.cu", "bwd.cu",
-           "gemv_sm100.cu", "api_ops.cu", "quantize.cu", "gemm_i8.cu", "gemm_i8_sm100.cu", "unpermute.cu"]
+           "gemv_sm100.cu", "api_ops.cu", "quantize.cu", "gemm_i8_sm100.cu", "unpermute.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
           "--expt-relaxed-constexpr"]

@@ -19,15 +19,18 @@ I8Layout make_i8_layout(const moe_problem& p) {
     };
     L.blockcnt = take(E * kk * NB * 4);
     L.blockoff = take(E * kk * NB * 4);
+    // sums of up to a grid of tail tiles: 256 channels by the rows of a tile
+    const long long rows = permuted_rows(p);
+    L.part_rows = (int)(rows < 128 ? (rows + 15) / 16 * 16 : 128);
+    L.part = take((size_t)kI8MaxGrid * 256 * L.part_rows * 4);
+    L.sem = take((size_t)kI8MaxGrid * 4 * 4);
     L.status = take(4);
     L.total = off;
     return L;
 }
 
 I8Form i8_form(const moe_problem& p) {
-    const long long rows = permuted_rows(p);
-    if (rows <= 16) return I8_STREAM;
-    return rows >= 256LL * p.E ? I8_PAIR : I8_SINGLE;
+    return permuted_rows(p) >= 256LL * p.E ? I8_PAIR : I8_SINGLE;
 }
 
 }  // namespace moe
@@ -85,8 +88,8 @@ int run_i8(const moe_problem* p, const int8_t* A, const float* sa, const int32_t
     g.out = out; g.out_dtype = p->dtype; g.N = N; g.K = K; g.rows = (int)permuted_rows(*p);
     g.status = stats ? static_cast<int32_t*>(stats) : reinterpret_cast<int32_t*>(ws + L.status);
     g.form = i8_form(*p);
-    CK(g.form == I8_STREAM ? launch_i8_gemm(g, static_cast<cudaStream_t>(stream))
-                           : launch_i8_tc(g, static_cast<cudaStream_t>(stream)));
+    g.part = reinterpret_cast<int*>(ws + L.part); g.sem = reinterpret_cast<int*>(ws + L.sem); g.part_rows = L.part_rows;
+    CK(launch_i8_tc(g, static_cast<cudaStream_t>(stream)));
     return MOE_OK;
 }
 

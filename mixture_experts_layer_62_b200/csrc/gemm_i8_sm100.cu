@@ -17,8 +17,8 @@
 //  * pair: clusters of two CTAs share 256 x 256 tiles (M = 256, cta_group::2):
 //    each loads 128 rows of A and half of the weight rows, which halves the
 //    shared-memory traffic of the weights; groups of many rows.
-//  * single: 128 x 256 tiles, the rows of A in boxes of 32 so that a group of
-//    few rows loads only what it has; the weights bound it.
+//  * single: one CTA a tile of 256 weight rows and up to 128 rows of A, for
+//    groups of few rows: the weights bound it.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -68,6 +68,8 @@ struct KP {
     int32_t* status;
     long long timeout_ns, drain_ns;
     int E, N, K, rows, nt, band_m;
+    int *part, *sem;   // single form: parts of the tail tiles [slots][part_rows][256] and arrivals [tail][4]
+    int part_rows;
 };
 
 template <int STAGES>
@@ -108,7 +110,10 @@ __device__ __forceinline__ void list_tiles(Ctl<STAGES>* c, const KP& p, int tile
         base += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) c->cum[p.E] = base;
-    if (kDebugChecks && __any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) debug_record_bounds(p.status);
+    if (kDebugChecks && __any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) {
+        pdl_wait();
+        debug_record_bounds(p.status);
+    }
 }
 
 struct Tile {
@@ -151,6 +156,7 @@ __device__ __forceinline__ bool wait_i8(uint64_t* bar, uint32_t parity, C* ctl, 
         if (global_timer_ns() - t0 > static_cast<uint64_t>(p.timeout_ns)) {
             *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
             if (peer_abort) st_shared_remote_u32(peer_abort, 1u);
+            pdl_wait();   // the status word has been reset by then
             atomicExch(p.status, MOE_ERR_TIMEOUT);
             return false;
         }
@@ -161,6 +167,7 @@ __device__ __forceinline__ void drain_i8(uint64_t* bar, uint32_t parity, const K
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(bar, parity))
         if (global_timer_ns() - t0 > static_cast<uint64_t>(p.drain_ns)) {
+            pdl_wait();
             atomicExch(p.status, MOE_ERR_TIMEOUT);
             return;
         }
@@ -408,6 +415,84 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 }
 
 // ---- single form ----------------------------------------------------------------
+// The weights are the M operand: a tile is 256 weight rows (two MMAs of M =
+// 128: SWIGLU 128 channels of B0 and the same of B1, PLAIN 256 channels of
+// B0) against up to 128 rows of A as N = 16, 32, .. 128, so a group of few
+// rows costs few tensor cycles and few bytes beside its weights, and a
+// thread of the epilogue owns a channel: its two scales are loaded once and
+// every store of a warp is 32 consecutive channels of one row.
+//
+// Units: the tiles that fill whole waves of the grid run one to a CTA, in
+// order, over all of K. The tail tiles are cut along K into equal shares for
+// all CTAs and run first, so that joining their parts hides under the whole
+// tiles: each part is added to the tile's accumulators in the workspace
+// (integer additions in L2, whose order does not matter), and the warp that
+// arrives last applies the scales and stores.
+struct Unit {
+    int tile, kb0, kb1;
+    int parts;        // contributors of the tile
+    int tail;         // index of the tile among the tail tiles
+};
+struct Units {
+    int whole, tail, nkb, grid, n;   // whole tiles of a CTA; tail tiles; K blocks a tile; CTAs; CTAs sharing the tail
+    __device__ __forceinline__ int lo(int b) const {
+        return static_cast<int>(static_cast<long long>(tail) * nkb * b / n);
+    }
+    __device__ __forceinline__ int owner(int r) const {   // the b with lo(b) <= r < lo(b + 1)
+        return static_cast<int>((static_cast<long long>(r + 1) * n - 1) / (static_cast<long long>(tail) * nkb));
+    }
+};
+constexpr int kMinShare = 4;   // K blocks: shorter shares cost more in joining than they save
+__device__ __forceinline__ Units units_of(int tiles, int nkb, int grid) {
+    Units u;
+    u.grid = grid;
+    u.nkb = nkb;
+    u.whole = tiles / grid;
+    u.tail = tiles - u.whole * grid;
+    const int shares = static_cast<int>((static_cast<long long>(u.tail) * nkb + kMinShare - 1) / kMinShare);
+    u.n = max(min(grid, max(shares, u.tail)), 1);
+    return u;
+}
+// Unit i of CTA b; false past the last.
+__device__ __forceinline__ bool unit_at(const Units& u, int b, int i, Unit& o) {
+    if (u.tail > 0 && b < u.n) {
+        const int r0 = u.lo(b), r1 = u.lo(b + 1), t0 = r0 / u.nkb;
+        const int cnt = r1 > r0 ? (r1 - 1) / u.nkb - t0 + 1 : 0;
+        if (i < cnt) {
+            const int t = t0 + i;
+            o.tail = t;
+            o.tile = u.whole * u.grid + t;
+            o.kb0 = max(r0 - t * u.nkb, 0);
+            o.kb1 = min(r1 - t * u.nkb, u.nkb);
+            o.parts = u.owner((t + 1) * u.nkb - 1) - u.owner(t * u.nkb) + 1;
+            return true;
+        }
+        i -= cnt;
+    }
+    if (i >= u.whole) return false;
+    o.tile = b + i * u.grid; o.kb0 = 0; o.kb1 = u.nkb; o.parts = 1; o.tail = 0;
+    return true;
+}
+
+// sixteen consecutive columns of this thread's TMEM lane, at two places
+__device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, uint32_t (&a)[16], uint32_t (&b)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
+          "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(b[0]),
+          "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]),
+          "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
+        : "r"(t0), "r"(t1)
+        : "memory");
+}
+__device__ __forceinline__ void red_add(int* p, uint32_t v) {
+    asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
 template <bool SWIGLU, typename OutT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
@@ -417,6 +502,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     using C = Ctl<S_STAGES>;
     C* ctl = reinterpret_cast<C*>(smem + S_STAGES * S_STAGE_BYTES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = static_cast<int>(blockIdx.x);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S_STAGES; ++s) {
@@ -437,27 +523,30 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                      ::"r"(smem_u32(&ctl->tmem_base)), "r"(TMEM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    // what this call's first launch writes (the status word and the arrival
+    // counters) is touched only after the wait at the epilogue's start or by
+    // a wait that gave up; all else was complete before that launch began
     if (warp == 2) list_tiles(ctl, p, BM);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = ctl->tmem_base;
-    const int units = ctl->cum[p.E];
-    const int num_kb = (p.K + BKB - 1) / BKB;
+    const Units un = units_of(ctl->cum[p.E], (p.K + BKB - 1) / BKB, static_cast<int>(gridDim.x));
 
     if (warp == 0) {
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0, armed = 0, armed_ph = 0;
             bool aborted = false;
-            for (int u = blockIdx.x; u < units && !aborted; u += gridDim.x) {
-                const Tile t = tile_of(ctl, p, u, BM);
+            Unit w;
+            for (int i = 0; !aborted && unit_at(un, b, i, w); ++i) {
+                const Tile t = tile_of(ctl, p, w.tile, BM);
                 const int arow = t.row0 + t.m_blk * BM;
                 const int boxes = (min(t.rows - t.m_blk * BM, BM) + 31) / 32;
                 const int brow = t.g * p.N + (SWIGLU ? t.n_blk * 128 : t.n_blk * 256);
                 const int brow1 = SWIGLU ? brow : brow + 128;
                 const CUtensorMap* mb1 = SWIGLU ? &tmB1 : &tmB0;
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     if (!wait_i8(&ctl->empty[s], ph ^ 1u, ctl, p)) { aborted = true; break; }
                     const uint32_t sa = smem_u32(smem + s * S_STAGE_BYTES);
                     mbar_arrive_expect_tx(&ctl->full[s], 2 * BH_BYTES + boxes * 32 * BKB);
@@ -465,8 +554,8 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
                     tma_load_2d(sa + A_BYTES, &tmB0, &ctl->full[s], kb * BKB, brow);
                     tma_load_2d(sa + A_BYTES + BH_BYTES, mb1, &ctl->full[s], kb * BKB, brow1);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(sa + b * 32 * BKB, &tmA, &ctl->full[s], kb * BKB, arow + 32 * b);
+                    for (int q = 0; q < boxes; ++q)
+                        tma_load_2d(sa + q * 32 * BKB, &tmA, &ctl->full[s], kb * BKB, arow + 32 * q);
                     if (++s == S_STAGES) { s = 0; ph ^= 1u; }
                 }
             }
@@ -479,20 +568,24 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             int s = 0, acc = 0;
             uint32_t ph = 0, aph = 0;
             bool aborted = false, issued = false;
-            for (int u = blockIdx.x; u < units && !aborted; u += gridDim.x) {
+            Unit w;
+            for (int i = 0; !aborted && unit_at(un, b, i, w); ++i) {
+                const Tile t = tile_of(ctl, p, w.tile, BM);
+                const uint32_t id = idesc_i8(BM, (min(t.rows - t.m_blk * BM, BM) + 15) / 16 * 16);
                 if (!wait_i8(&ctl->tempty[acc], aph ^ 1u, ctl, p)) { aborted = true; break; }
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(acc * ACC_COLS);
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     if (!wait_i8(&ctl->full[s], ph, ctl, p)) { aborted = true; break; }
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + s * S_STAGE_BYTES);
-                    // rows of A that no box brought are whatever the stage held: their
-                    // accumulator rows are never stored
-                    const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + A_BYTES);
+                    const uint64_t xd = sw128_desc(sa), w0 = sw128_desc(sa + A_BYTES), w1 = sw128_desc(sa + A_BYTES + BH_BYTES);
 #pragma unroll
-                    for (int kk = 0; kk < BKB / 32; ++kk)
-                        mma_i8(d, ad + 2u * kk, bd + 2u * kk, idesc_i8(BM, 256), (kb | kk) != 0 ? 1u : 0u);
+                    for (int kk = 0; kk < BKB / 32; ++kk) {
+                        const uint32_t accum = kb != w.kb0 || kk != 0 ? 1u : 0u;
+                        mma_i8(d, w0 + 2u * kk, xd + 2u * kk, id, accum);
+                        mma_i8(d + 128u, w1 + 2u * kk, xd + 2u * kk, id, accum);
+                    }
                     issued = true;
                     tc_commit(&ctl->empty[s]);
                     if (++s == S_STAGES) { s = 0; ph ^= 1u; }
@@ -508,22 +601,76 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             }
         }
     } else {
-        const int q = warp & 3;
-        const int r = q * 32 + lane;
+        const int q = warp & 3, r = q * 32 + lane;   // this thread's channel of each half
         int acc = 0;
         uint32_t aph = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x) {
-            const Tile t = tile_of(ctl, p, u, BM);
-            const int grow = t.m_blk * BM + r;
-            const bool valid = grow < t.rows;
-            const size_t orow = static_cast<size_t>(t.row0) + static_cast<size_t>(grow);
-            const float sa = valid ? p.sa[orow] : 0.f;
+        pdl_wait();
+        OutT* out = static_cast<OutT*>(p.out);
+        Unit w;
+        for (int i = 0; unit_at(un, b, i, w); ++i) {
+            const Tile t = tile_of(ctl, p, w.tile, BM);
+            int nrow = min(t.rows - t.m_blk * BM, BM);
+            const size_t row0 = static_cast<size_t>(t.row0) + static_cast<size_t>(t.m_blk) * BM;
+            const int ch0 = (SWIGLU ? t.n_blk * 128 : t.n_blk * 256) + r, ch1 = SWIGLU ? ch0 : ch0 + 128;
+            const size_t sc = static_cast<size_t>(t.g) * p.N;
+            const float f0 = ch0 < p.N ? p.sb0[sc + ch0] : 0.f;
+            const float f1 = ch1 < p.N ? (SWIGLU ? p.sb1 : p.sb0)[sc + ch1] : 0.f;
+            float sa_l[4];   // row scales: lane l holds rows l, 32 + l, 64 + l, 96 + l
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sa_l[j] = 32 * j + lane < nrow ? p.sa[row0 + 32 * j + lane] : 0.f;
             if (!wait_i8(&ctl->tfull[acc], aph, ctl, p)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * ACC_COLS);
-            if (t.m_blk * BM + q * 32 < t.rows) {   // the warp has a row
-                if (SWIGLU) store_cols<true, OutT>(p, tb, 128, 128, t.n_blk * 128, t.g, valid, orow, sa);
-                else store_cols<false, OutT>(p, tb, 0, 256, t.n_blk * 256, t.g, valid, orow, sa);
+            int* sums = p.part + static_cast<size_t>(w.tail) * 256 * p.part_rows + r;   // [row][256 channels]
+            if (w.parts > 1) {
+#pragma unroll 1
+                for (int c = 0; c < nrow; c += 16) {
+                    uint32_t lo[16], hi[16];
+                    tmem_ld16x2(tb + c, tb + 128 + c, lo, hi);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c + j < nrow) {
+                            red_add(sums + (c + j) * 256, lo[j]);
+                            red_add(sums + (c + j) * 256 + 128, hi[j]);
+                        }
+                }
+                __threadfence();
+                __syncwarp();
+                int old = 0;
+                if (lane == 0) old = atomicAdd(p.sem + w.tail * 4 + q, 1);
+                old = __shfl_sync(0xffffffffu, old, 0);
+                __threadfence();
+                if (old != w.parts - 1) nrow = 0;   // another part comes later: its warp finishes
+            }
+            {
+#pragma unroll 1
+                for (int c = 0; c < nrow; c += 16) {
+                    uint32_t lo[16], hi[16];
+                    if (w.parts == 1) {
+                        tmem_ld16x2(tb + c, tb + 128 + c, lo, hi);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            lo[j] = c + j < nrow ? static_cast<uint32_t>(__ldcg(sums + (c + j) * 256)) : 0u;
+                            hi[j] = c + j < nrow ? static_cast<uint32_t>(__ldcg(sums + (c + j) * 256 + 128)) : 0u;
+                        }
+                    }
+                    const float sa_c = c < 32 ? sa_l[0] : c < 64 ? sa_l[1] : c < 96 ? sa_l[2] : sa_l[3];
+                    OutT* o = out + (row0 + c) * p.N;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float sa = __shfl_sync(0xffffffffu, sa_c, (c & 16) + j);
+                        const bool in = c + j < nrow;
+                        const float y0 = static_cast<float>(static_cast<int>(lo[j])) * sa * f0;
+                        const float y1 = static_cast<float>(static_cast<int>(hi[j])) * sa * f1;
+                        if (SWIGLU) {
+                            if (in && ch0 < p.N) put(o + static_cast<size_t>(j) * p.N + ch0, silu(y0, out) * y1);
+                        } else {
+                            if (in && ch0 < p.N) put(o + static_cast<size_t>(j) * p.N + ch0, y0);
+                            if (in && ch1 < p.N) put(o + static_cast<size_t>(j) * p.N + ch1, y1);
+                        }
+                    }
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -539,6 +686,28 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
                      : "memory");
+    }
+}
+
+// First launch of a product: the status word is MOE_OK, and the arrival
+// counters and accumulators of the tail tiles are zero, before any CTA of the
+// product touches them. The product starts beside it (it needs nothing of
+// this until its own wait).
+__global__ void __launch_bounds__(256) i8_begin_kernel(const KP p, int grid) {
+    __shared__ Ctl<1> c;
+    pdl_launch();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = MOE_OK;
+    if (p.part == nullptr) return;
+    if (threadIdx.x < 32) list_tiles(&c, p, BM);
+    __syncthreads();
+    const Units u = units_of(c.cum[p.E], (p.K + BKB - 1) / BKB, grid);
+    if (u.n <= u.tail) return;   // no tile has more than one part
+    for (int t = blockIdx.x; t < u.tail; t += gridDim.x) {
+        const Tile tile = tile_of(&c, p, u.whole * u.grid + t, BM);
+        const int n = min(tile.rows - tile.m_blk * BM, BM) * 64;
+        int4* part = reinterpret_cast<int4*>(p.part + static_cast<size_t>(t) * 256 * p.part_rows);
+        for (int i = threadIdx.x; i < n; i += 256) part[i] = make_int4(0, 0, 0, 0);
+        if (threadIdx.x < 4) p.sem[t * 4 + threadIdx.x] = 0;
     }
 }
 
@@ -579,13 +748,11 @@ cudaError_t launch_tc(Kernel kernel, size_t smem, int grid, const CUtensorMap& a
 template <bool SWIGLU, typename OutT>
 cudaError_t launch_form(const I8Gemm& g, const KP& kp, const CUtensorMap& a, const CUtensorMap& b0,
                         const CUtensorMap& b1, cudaStream_t st) {
-    const int sms = device_sm_count();
-    if (sms < 2) return cudaErrorInvalidDevice;
     if (g.form == I8_PAIR)
         return launch_tc(i8_pair_kernel<SWIGLU, OutT>, P_STAGES * P_STAGE_BYTES + 1024 + sizeof(Ctl<P_STAGES>),
-                         sms & ~1, a, b0, b1, kp, st);
-    return launch_tc(i8_single_kernel<SWIGLU, OutT>, S_STAGES * S_STAGE_BYTES + 1024 + sizeof(Ctl<S_STAGES>), sms, a,
-                     b0, b1, kp, st);
+                         device_sm_count() & ~1, a, b0, b1, kp, st);
+    return launch_tc(i8_single_kernel<SWIGLU, OutT>, S_STAGES * S_STAGE_BYTES + 1024 + sizeof(Ctl<S_STAGES>),
+                     std::min(device_sm_count(), kI8MaxGrid), a, b0, b1, kp, st);
 }
 
 }  // namespace
@@ -605,8 +772,15 @@ cudaError_t launch_i8_tc(const I8Gemm& g, cudaStream_t st) {
     kp.nt = ceil_div(g.N, swiglu ? 128 : 256);
     const long long blk = static_cast<long long>(pair ? 256 : BM) * g.K;
     kp.band_m = static_cast<int>(std::max(8ll, kBandBytes / blk));
-    cudaError_t e = cudaMemsetAsync(g.status, 0, sizeof(int32_t), st);   // MOE_OK before any CTA can report
+    if (!pair) { kp.part = g.part; kp.sem = g.sem; kp.part_rows = g.part_rows; }
+    const int grid = std::min(device_sm_count(), kI8MaxGrid);
+    if (grid < 2) return cudaErrorInvalidDevice;
+    cudaError_t e = launch_k(i8_begin_kernel, dim3(pair ? 1 : grid), dim3(256), 0, st, kp, grid);
     if (e != cudaSuccess) return e;
+    struct Dependent {   // the product is launched as a programmatic dependent of it
+        Dependent() { g_pdl = true; }
+        ~Dependent() { g_pdl = false; }
+    } dependent;
     if (g.out_dtype == MOE_DTYPE_BF16)
         return swiglu ? launch_form<true, __nv_bfloat16>(g, kp, a, b0, b1, st)
                       : launch_form<false, __nv_bfloat16>(g, kp, a, b0, b1, st);

@@ -12,13 +12,16 @@ namespace moe {
 // Byte offsets of moe_int8_workspace_size(p) bytes.
 struct I8Layout {
     size_t blockcnt, blockoff;   // permutation: per-chunk expert counts and their scan
+    size_t part, sem;            // products: sums and arrival counters of the tail tiles
+    int part_rows;               // rows of a tile's sums
     size_t status;               // status word of a call without a statistics block
     size_t total;
 };
 I8Layout make_i8_layout(const moe_problem& p);
 
 // One product of the experts: out[r][n] over the rows of every group.
-enum I8Form { I8_STREAM = 0, I8_SINGLE = 1, I8_PAIR = 2 };
+enum I8Form { I8_SINGLE = 0, I8_PAIR = 1 };
+constexpr int kI8MaxGrid = 160;   // CTAs of the single form at most: sizes the workspace on any host
 I8Form i8_form(const moe_problem& p);
 struct I8Gemm {
     int form;
@@ -34,8 +37,9 @@ struct I8Gemm {
     int out_dtype;
     int N, K, rows;
     int32_t* status;
+    int *part, *sem;         // single form: sums of the tail tiles and their arrival counters
+    int part_rows;
 };
-cudaError_t launch_i8_gemm(const I8Gemm& g, cudaStream_t st);
 cudaError_t launch_i8_tc(const I8Gemm& g, cudaStream_t st);
 
 // rows of x -> q, scale; only the first min(rows, *used) rows when used != null
