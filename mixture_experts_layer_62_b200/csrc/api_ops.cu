@@ -131,20 +131,14 @@ int moe_permute_int8(const moe_problem* p, const void* x, const int32_t* idx, in
         return MOE_OK;
     }
     char* ws = static_cast<char*>(workspace);
-    int32_t* blockcnt = reinterpret_cast<int32_t*>(ws + L.blockcnt);
-    int32_t* blockoff = reinterpret_cast<int32_t*>(ws + L.blockoff);
-    const int kk = count_slots(*p);
-    CK(launch_hist(idx, p->T, p->k, kk, p->E, blockcnt, st));
-    ScanArgs sa = {};
-    sa.T = p->T; sa.k = p->k; sa.E = p->E; sa.capacity = C; sa.kk = kk;
-    sa.blockcnt = blockcnt; sa.blockoff = blockoff;
-    sa.indptr = indptr; sa.stats = stats;
-    sa.pad = p->pad_rows;
-    CK(launch_scan(sa, st));
-    CK(launch_permute_gather(p->dtype, nullptr, idx, blockoff, indptr, p->T, p->d, p->E, p->k, kk, C, pos, row_token,
-                             nullptr, st));
-    CK(launch_quantize_scatter(p->dtype, x, pos, p->T, p->d, p->k, (int)permuted_rows(*p), xq, xs, st));
-    if (p->pad_rows > 0) CK(launch_pad_rows_i8(indptr, stats, p->E, p->d, xq, xs, row_token, p->pad_rows, st));
+    PermuteI8 a = {};
+    a.dtype = p->dtype; a.x = x; a.idx = idx;
+    a.blockcnt = reinterpret_cast<int32_t*>(ws + L.blockcnt);
+    a.blockoff = reinterpret_cast<int32_t*>(ws + L.blockoff);
+    a.pos = pos; a.indptr = indptr; a.row_token = row_token; a.xq = xq; a.xs = xs; a.stats = stats;
+    a.T = p->T; a.d = p->d; a.E = p->E; a.k = p->k; a.kk = count_slots(*p); a.capacity = C; a.pad = p->pad_rows;
+    a.rows = (int)permuted_rows(*p);
+    CK(launch_permute_i8(a, st));
     return MOE_OK;
 }
 

@@ -45,12 +45,19 @@ cudaError_t launch_i8_tc(const I8Gemm& g, cudaStream_t st);
 // rows of x -> q, scale; only the first min(rows, *used) rows when used != null
 cudaError_t launch_quantize_rows(int dtype, const void* x, int rows, int cols, const int32_t* used, int8_t* q,
                                  float* scale, cudaStream_t st);
-// the rows of x [T, d], each to its kept destinations pos[t, :]
-cudaError_t launch_quantize_scatter(int dtype, const void* x, const int32_t* pos, int T, int d, int k, int rows,
-                                    int8_t* xq, float* xs, cudaStream_t st);
-// zeros in the padding rows (row_token < 0) of [0, indptr[E])
-cudaError_t launch_pad_rows_i8(const int32_t* indptr, const void* stats, int E, int d, int8_t* xq, float* xs,
-                               int32_t* row_token, int pad, cudaStream_t st);
+// the permutation of moe_permute with the rows in 8 bits
+struct PermuteI8 {
+    int dtype;
+    const void* x;
+    const int32_t* idx;
+    int32_t *blockcnt, *blockoff;   // workspace: per-chunk expert counts and their scan
+    int32_t *pos, *indptr, *row_token;
+    int8_t* xq;
+    float* xs;
+    void* stats;
+    int T, d, E, k, kk, capacity, pad, rows;
+};
+cudaError_t launch_permute_i8(const PermuteI8& a, cudaStream_t st);
 
 // ---- the way back -----------------------------------------------------------
 

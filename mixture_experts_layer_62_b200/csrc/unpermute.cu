@@ -94,71 +94,63 @@ __device__ __forceinline__ void drop8(const Dropout& d, unsigned long long seed,
     }
 }
 
-constexpr int kMixWarps = 8;
-
-// One warp per (token, 32 consecutive vectors of the row): lane j holds the
-// position and gate of slot j, every lane one vector of eight columns; the
-// rows of up to four slots are requested before the first is added.
-template <typename T, bool GATED, bool DROP>
-__global__ void __launch_bounds__(kMixWarps * 32)
+// A block takes a token (or one of a few stretches of its row, for small
+// batches): its positions and gates are loaded once, and each thread walks
+// vectors of eight columns, the rows of all K slots requested together
+// (K: k rounded up to 1, 2, 4, 8 or 16).
+constexpr int kMixThreads = 128;
+template <typename T, bool GATED, bool DROP, int K>
+__global__ void __launch_bounds__(kMixThreads)
 mix_kernel(const __grid_constant__ MixArgs a, int slices) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long task = static_cast<long long>(blockIdx.x) * kMixWarps + warp;
-    const long long t = task / slices;
-    if (t >= a.T) return;
-    const int sl = static_cast<int>(task - t * slices);
-    int p_l = -1;
-    float g_l = 1.f;
-    if (lane < a.k) {
-        p_l = a.pos[t * a.k + lane];
-        if (GATED) g_l = a.gate[t * a.k + lane];
-        if (p_l >= a.rows) p_l = -1;   // not a row of o: the slot is skipped
+    const size_t t = blockIdx.x / slices;
+    const int sl = static_cast<int>(blockIdx.x - t * slices), nvec = a.d / 8;
+    const int v_lo = static_cast<int>(static_cast<long long>(nvec) * sl / slices);
+    const int v_hi = static_cast<int>(static_cast<long long>(nvec) * (sl + 1) / slices);
+    int p[K];
+    float g[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        p[j] = j < a.k ? a.pos[t * a.k + j] : -1;
+        g[j] = GATED && j < a.k ? a.gate[t * a.k + j] : 1.f;
+        if (p[j] >= a.rows) p[j] = -1;   // not a row of o: the slot is skipped
     }
-    const int v = sl * 32 + lane;
-    const bool on = v < a.d / 8;
-    const size_t col = static_cast<size_t>(v) * 8;
+    unsigned long long seed = 0, offset = 0;
+    if (DROP) {
+        seed = a.drop.rng[0];
+        offset = a.drop.rng[1];
+    }
     const T* o = static_cast<const T*>(a.o);
-    const size_t at = static_cast<size_t>(t) * a.d + col;
-    Vec8<T> rv, sv;
-    if (on && a.residual != nullptr) rv.load(static_cast<const T*>(a.residual) + at);
-    if (on && a.s != nullptr) sv.load(static_cast<const T*>(a.s) + at);
-    float acc[8];
+    for (int v = v_lo + static_cast<int>(threadIdx.x); v < v_hi; v += kMixThreads) {
+        const size_t col = static_cast<size_t>(v) * 8, at = t * a.d + col;
+        Vec8<T> raw[K], rv, sv;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    for (int j0 = 0; j0 < a.k; j0 += 4) {
-        Vec8<T> raw[4];
-        int pj[4];
+        for (int j = 0; j < K; ++j)
+            if (p[j] >= 0) raw[j].load(o + static_cast<size_t>(p[j]) * a.d + col);
+        if (a.s != nullptr) sv.load(static_cast<const T*>(a.s) + at);
+        if (a.residual != nullptr) rv.load(static_cast<const T*>(a.residual) + at);
+        float acc[8], x[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            // lanes of k and above hold -1; MOE_MAX_K = 16 keeps j0 + u below 32
-            pj[u] = __shfl_sync(0xffffffffu, p_l, j0 + u);
-            if (pj[u] >= 0 && on) raw[u].load(o + static_cast<size_t>(pj[u]) * a.d + col);
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            if (p[j] < 0) continue;
+            raw[j].get(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = GATED ? fmaf(g[j], x[e], acc[e]) : acc[e] + x[e];
         }
+        if (a.s != nullptr) {
+            sv.get(x);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float g = __shfl_sync(0xffffffffu, g_l, j0 + u);
-            if (pj[u] >= 0 && on) {
-                float x[8];
-                raw[u].get(x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = GATED ? fmaf(g, x[e], acc[e]) : acc[e] + x[e];
-            }
+            for (int e = 0; e < 8; ++e) acc[e] += x[e];
         }
-    }
-    if (!on) return;
-    float x[8];
-    if (a.s != nullptr) {
-        sv.get(x);
+        if (DROP) drop8(a.drop, seed, offset, static_cast<unsigned long long>(at / 8), acc);
+        if (a.residual != nullptr) {
+            rv.get(x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += x[e];
+            for (int e = 0; e < 8; ++e) acc[e] += x[e];
+        }
+        Vec8<T>::store(static_cast<T*>(a.out) + at, acc);
     }
-    if (DROP) drop8(a.drop, a.drop.rng[0], a.drop.rng[1], static_cast<unsigned long long>(at / 8), acc);
-    if (a.residual != nullptr) {
-        rv.get(x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += x[e];
-    }
-    Vec8<T>::store(static_cast<T*>(a.out) + at, acc);
 }
 
 // One block per token: a thread takes every THREADS-th vector of dy, forms
@@ -250,14 +242,22 @@ cudaError_t mix_back_t(const MixBackArgs& a, cudaStream_t st) {
     return mix_back_k<T, DROP, 16>(a, st);
 }
 
+template <typename T, bool GATED, bool DROP>
+cudaError_t mix_d(const MixArgs& a, cudaStream_t st) {
+    // fewer tokens than two blocks an SM: stretches of the rows, a pass of the threads at least
+    int slices = 1;
+    while (a.T * slices < 2 * 148 && slices * kMixThreads < a.d / 8) slices *= 2;
+    const dim3 grid(static_cast<unsigned>(a.T) * slices), block(kMixThreads);
+    if (a.k <= 1) return launch_k(mix_kernel<T, GATED, DROP, 1>, grid, block, 0, st, a, slices);
+    if (a.k <= 2) return launch_k(mix_kernel<T, GATED, DROP, 2>, grid, block, 0, st, a, slices);
+    if (a.k <= 4) return launch_k(mix_kernel<T, GATED, DROP, 4>, grid, block, 0, st, a, slices);
+    if (a.k <= 8) return launch_k(mix_kernel<T, GATED, DROP, 8>, grid, block, 0, st, a, slices);
+    return launch_k(mix_kernel<T, GATED, DROP, 16>, grid, block, 0, st, a, slices);
+}
 template <typename T>
 cudaError_t mix_t(const MixArgs& a, cudaStream_t st) {
-    const int slices = ceil_div(a.d / 8, 32);
-    const long long tasks = static_cast<long long>(a.T) * slices;
-    const dim3 grid(static_cast<unsigned>((tasks + kMixWarps - 1) / kMixWarps)), block(kMixWarps * 32);
-    if (a.gate == nullptr) return launch_k(mix_kernel<T, false, false>, grid, block, 0, st, a, slices);
-    if (a.drop.rng == nullptr) return launch_k(mix_kernel<T, true, false>, grid, block, 0, st, a, slices);
-    return launch_k(mix_kernel<T, true, true>, grid, block, 0, st, a, slices);
+    if (a.gate == nullptr) return mix_d<T, false, false>(a, st);
+    return a.drop.rng == nullptr ? mix_d<T, true, false>(a, st) : mix_d<T, true, true>(a, st);
 }
 
 }  // namespace
