@@ -14,9 +14,9 @@
 // each CTA's shared memory from the group offsets. Every wait is bounded
 // (moe_set_wait_limit): on expiry the CTA records MOE_ERR_TIMEOUT, lets what
 // it started land, frees its tensor memory and returns.
-//  * pair: clusters of two CTAs share 256 x 256 tiles (M = 256, cta_group::2):
-//    each loads 128 rows of A and half of the weight rows, which halves the
-//    shared-memory traffic of the weights; groups of many rows.
+//  * pair: clusters of two CTAs share tiles of 256 rows of A x 256 weight
+//    rows (cta_group::2), each CTA loading half of both, which halves the
+//    bytes a CTA brings in for the same products; groups of many rows.
 //  * single: one CTA a tile of 256 weight rows and up to 128 rows of A, for
 //    groups of few rows: the weights bound it.
 #include <cuda.h>
@@ -39,7 +39,10 @@ constexpr int A_BYTES = BM * BKB;           // 16 KB
 constexpr int BH_BYTES = 128 * BKB;         // 128 weight rows, 16 KB
 constexpr int ACC_COLS = 256, TMEM_COLS = 512;
 constexpr int NUM_THREADS = 192;
-constexpr int P_STAGES = 6, P_STAGE_BYTES = A_BYTES + BH_BYTES;
+constexpr int P_STAGES = 4, P_STAGE_BYTES = A_BYTES + 2 * BH_BYTES;
+constexpr int P_THREADS = 320;                      // pair: eight epilogue warps
+constexpr int P_XCH_FLOATS = 4 * 2 * 16 * 32;       // pair SWIGLU: [warp pair][direction][16 rows][32 channels]
+constexpr int P_SCALE_FLOATS = 8 * 128;             // pair: the channel scales of each epilogue warp's columns
 constexpr int S_STAGES = 4, S_STAGE_BYTES = A_BYTES + 2 * BH_BYTES;
 constexpr long long kBandBytes = 32ll << 20;   // rows of A that a band of M blocks keeps in L2
 
@@ -142,7 +145,9 @@ __device__ __forceinline__ Tile tile_of(const Ctl<STAGES>* c, const KP& p, int i
         h = min(p.band_m, mt - m0);
     }
     t.n_blk = id / h;
-    t.m_blk = m0 + id % h;
+    // turned by one from each weight tile to the next, so that a CTA's units
+    // (a fixed stride apart) do not meet the short last block every time
+    t.m_blk = m0 + (id + t.n_blk) % h;
     return t;
 }
 
@@ -173,70 +178,108 @@ __device__ __forceinline__ void drain_i8(uint64_t* bar, uint32_t parity, const K
         }
 }
 
-// SiLU with the exponential of the output's precision
-__device__ __forceinline__ float silu(float a, float*) { return a / (1.f + expf(-a)); }
-__device__ __forceinline__ float silu(float a, __nv_bfloat16*) { return __fdividef(a, 1.f + __expf(-a)); }
+// ---- epilogue arithmetic -------------------------------------------------------
+// Two fp32 values an instruction (f32x2: each rounded as the scalar form).
+__device__ __forceinline__ uint64_t pk(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpk(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kNegLog2e = -1.4426950408889634f;
+// SiLU(a) b = (a / (1 + exp(-a))) b. bf16 results: the fast exponential and
+// reciprocal (a few 2^-23 off, where the type rounds to 2^-8); fp32 results:
+// the accurate ones. exp(-a) overflowing gives a 0, as it should. The scalar
+// and the two-value form take the same roundings.
+__device__ __forceinline__ float swiglu(float a, float b, float*) { return a / (1.f + expf(-a)) * b; }
+__device__ __forceinline__ float swiglu(float a, float b, __nv_bfloat16*) {
+    return __fmul_rn(__fmul_rn(a, rcp(__fadd_rn(1.f, ex2(__fmul_rn(a, kNegLog2e))))), b);
+}
+__device__ __forceinline__ uint64_t swiglu2(uint64_t a, uint64_t b, __nv_bfloat16*) {
+    const float2 t = unpk(mul2(a, pk(kNegLog2e, kNegLog2e)));
+    const float2 d = unpk(add2(pk(ex2(t.x), ex2(t.y)), pk(1.f, 1.f)));
+    return mul2(mul2(a, pk(rcp(d.x), rcp(d.y))), b);
+}
+__device__ __forceinline__ uint64_t swiglu2(uint64_t a, uint64_t b, float* o) {
+    const float2 x = unpk(a), y = unpk(b);
+    return pk(swiglu(x.x, y.x, o), swiglu(x.y, y.y, o));
+}
+// (float(sum) sa) sb for two sums
+__device__ __forceinline__ uint64_t scaled2(uint32_t s0, uint32_t s1, uint64_t sa, uint64_t sb) {
+    return mul2(mul2(pk(static_cast<float>(static_cast<int>(s0)), static_cast<float>(static_cast<int>(s1))), sa), sb);
+}
+__device__ __forceinline__ float scaled(uint32_t s, float sa, float sb) {
+    return __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(s)), sa), sb);
+}
 
-__device__ __forceinline__ void store16(float* p, const float (&v)[16]) {
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Sixteen results as 16-byte pieces (bf16: 2, fp32: 4) to piece p0 of row `row` of a warp's 32 x 64-byte stage: piece
+// p lies at p ^ ((row / 2) % 4), so that eight lanes fall on different banks both here and when rows are read back.
+__device__ __forceinline__ uint4* stage_at(uint8_t* st, int row, int p) {
+    return reinterpret_cast<uint4*>(st + row * 64 + ((p ^ ((row >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ void stage16(uint8_t* st, int row, int, const float (&v)[16], float*) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        *stage_at(st, row, i) = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                           __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
 }
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16]) {
+__device__ __forceinline__ void stage16(uint8_t* st, int row, int p0, const float (&v)[16], __nv_bfloat16*) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
         w[i] = *reinterpret_cast<uint32_t*>(&h);
     }
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-}
-
-// One accumulator row of this thread: columns [c0, c0 + n) of the gate (or
-// plain) accumulator at tb and, SWIGLU, of the up accumulator at tb + up;
-// output columns from col0. N is a multiple of 16, so 16 columns at a time.
-template <bool SWIGLU, typename OutT>
-__device__ __forceinline__ void store_cols(const KP& p, uint32_t tb, uint32_t up, int n, int col0, int g, bool valid,
-                                           size_t orow, float sa) {
-    OutT* out = static_cast<OutT*>(p.out) + orow * p.N;
-    const float* s0 = p.sb0 + static_cast<size_t>(g) * p.N;
-    const float* s1 = SWIGLU ? p.sb1 + static_cast<size_t>(g) * p.N : nullptr;
-#pragma unroll 1
-    for (int c = 0; c < n; c += 32) {
-        uint32_t a[32], b[SWIGLU ? 32 : 1];
-        tmem_ld32(tb + c, a);
-        if constexpr (SWIGLU) tmem_ld32(tb + up + c, b);
-#pragma unroll
-        for (int q = 0; q < 32; q += 16) {
-            const int col = col0 + c + q;
-            if (!valid || col >= p.N) continue;
-            float v[16];
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(s0 + col + i));
-                v[i] = static_cast<float>(static_cast<int>(a[q + i])) * sa * f.x;
-                v[i + 1] = static_cast<float>(static_cast<int>(a[q + i + 1])) * sa * f.y;
-                v[i + 2] = static_cast<float>(static_cast<int>(a[q + i + 2])) * sa * f.z;
-                v[i + 3] = static_cast<float>(static_cast<int>(a[q + i + 3])) * sa * f.w;
-                if constexpr (SWIGLU) {
-                    const float4 h = __ldg(reinterpret_cast<const float4*>(s1 + col + i));
-                    v[i] = silu(v[i], out) * (static_cast<float>(static_cast<int>(b[q + i])) * sa * h.x);
-                    v[i + 1] = silu(v[i + 1], out) * (static_cast<float>(static_cast<int>(b[q + i + 1])) * sa * h.y);
-                    v[i + 2] = silu(v[i + 2], out) * (static_cast<float>(static_cast<int>(b[q + i + 2])) * sa * h.z);
-                    v[i + 3] = silu(v[i + 3], out) * (static_cast<float>(static_cast<int>(b[q + i + 3])) * sa * h.w);
-                }
-            }
-            store16(out + col, v);
-        }
-    }
+    *stage_at(st, row, p0) = make_uint4(w[0], w[1], w[2], w[3]);
+    *stage_at(st, row, p0 + 1) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 // ---- pair form ----------------------------------------------------------------
-// Accumulator columns: SWIGLU [128 gate | 128 up] (rank 0's weight rows come
-// from B0, rank 1's from B1), PLAIN 256 output columns. The tiles that do not
-// fill a whole wave run as two half-width items each when that still fits in
-// one wave (64 columns of each half), so the last wave is half as long.
+// Whole tiles: the rows of A are the M operand (rank r holds rows [128 r, 128
+// r + 128)), 256 weight rows the N operand (SWIGLU: rank 0 brings 128 rows of
+// B0, rank 1 the same of B1, so the accumulator is [128 gates | 128 ups]).
+// Short tiles, of at most kShort rows (the ragged end of a group): the
+// weights are the M operand and the rows N = 32, 64, .., so they cost what
+// they hold. With whole tiles alone a group of 1030 rows pays for 1280: eight
+// experts of a random router lost 11 % that way. SWIGLU: rank r's M rows are
+// B0's and B1's rows of its 64 channels, so TMEM lanes 0..63 (epilogue warps
+// q = 0, 1) hold the gates and lanes 64..127 (q = 2, 3) the up values of the
+// same channels; warps q and q + 2 trade halves of every 32 columns through
+// shared memory: each sends 16, receives 16, and finishes 16 rows of its 32
+// channels. (That trade is why whole tiles are not laid out this way too:
+// its shared-memory traffic slows the products beside it, 731 us against
+// PAIRUP for the Mixtral-shaped up projection of 8192 rows.)
+// Eight warps share the epilogue, two to a quarter of the lanes.
+// The tiles that do not fill a whole wave run as two items of 128 rows each
+// when that still fits in one wave.
+constexpr int kShort = 192;
 struct Work {
     int full, items;
 };
@@ -248,26 +291,155 @@ __device__ __forceinline__ Work work_of(int units, int nclusters) {
     if (tail > 0 && 2 * tail <= nclusters) w.items = w.full + 2 * tail; else w.full = units;
     return w;
 }
-__device__ __forceinline__ int item_tile(const Work& w, int v, int& half) {
-    if (v < w.full) { half = -1; return v; }
-    half = (v - w.full) & 1;
-    return w.full + ((v - w.full) >> 1);
+struct Item {
+    Tile t;
+    size_t row0;   // first row of A
+    int n;         // rows of A (0: nothing to do)
+    bool shrt;     // a short tile: the weights are the M operand
+};
+template <typename C>
+__device__ __forceinline__ Item item_at(const C* c, const KP& p, const Work& w, int v) {
+    Item i;
+    const int half = v < w.full ? -1 : (v - w.full) & 1;
+    i.t = tile_of(c, p, v < w.full ? v : w.full + ((v - w.full) >> 1), 256);
+    const int lo = i.t.m_blk * 256 + (half > 0 ? 128 : 0);
+    i.n = max(min(i.t.rows - lo, half < 0 ? 256 : 128), 0);
+    i.shrt = i.n <= kShort;
+    i.row0 = static_cast<size_t>(i.t.row0) + static_cast<size_t>(lo);
+    return i;
+}
+// The two warps of an epilogue pair (64 threads): the logical and of `ok`.
+__device__ __forceinline__ bool pair_and(int id, bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.and.pred p, %2, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r) : "r"(ok ? 1u : 0u), "r"(id) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// Epilogues of one set by one warp (half h of its columns).
+// Whole tile: a thread is row r, columns are channels from ch0.
+// sc: the scales of the warp's columns in shared memory (SWIGLU 64 of B0,
+// then 64 of B1). The results go through a 2 KB stage of the warp, so that
+// every row is written in whole 64-byte runs: with each lane storing its own
+// row's 16 bytes the stores alone cost 36 of 435 us (4096 rows, K = 4096, 18944
+// channels).
+template <bool SWIGLU, typename OutT>
+__device__ __forceinline__ void whole_tile(const KP& p, const Item& it, uint32_t tb, int h, int r0, int ch0, float sa,
+                                           const float* sc, uint8_t* stage, OutT* out) {
+    const int lane = threadIdx.x & 31;
+    constexpr int HALF = SWIGLU ? 64 : 128;
+    constexpr int RUN = 64 / sizeof(OutT);   // channels of a 64-byte run
+    constexpr int PER = 16 / sizeof(OutT);   // channels of a piece
+    const uint64_t sa2 = pk(sa, sa);
+#pragma unroll 1
+    for (int c = 0; c < HALF; c += 32) {
+        uint32_t a[32], b[SWIGLU ? 32 : 1];
+        tmem_ld32(tb + HALF * h + c, a);
+        if constexpr (SWIGLU) tmem_ld32(tb + 128 + HALF * h + c, b);
+#pragma unroll
+        for (int e = 0; e < 32; e += 16) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const ulonglong2 s0 = *reinterpret_cast<const ulonglong2*>(sc + c + e + i);
+                uint64_t y0 = scaled2(a[e + i], a[e + i + 1], sa2, s0.x), y1 = scaled2(a[e + i + 2], a[e + i + 3], sa2, s0.y);
+                if constexpr (SWIGLU) {
+                    const ulonglong2 s1 = *reinterpret_cast<const ulonglong2*>(sc + 64 + c + e + i);
+                    y0 = swiglu2(y0, scaled2(b[e + i], b[e + i + 1], sa2, s1.x), out);
+                    y1 = swiglu2(y1, scaled2(b[e + i + 2], b[e + i + 3], sa2, s1.y), out);
+                }
+                const float2 f0 = unpk(y0), f1 = unpk(y1);
+                v[i] = f0.x; v[i + 1] = f0.y; v[i + 2] = f1.x; v[i + 3] = f1.y;
+            }
+            stage16(stage, lane, (e / PER) & 3, v, out);
+            if ((e + 16) % RUN == 0) {
+                __syncwarp();
+                const int ch = ch0 + HALF * h + c + e + 16 - RUN + (lane & 3) * PER;
+                if (ch < p.N) {   // N is a multiple of 16: pieces are in or out
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = i * 8 + (lane >> 2);
+                        if (r0 + row < it.n)
+                            *reinterpret_cast<uint4*>(out + (it.row0 + r0 + row) * p.N + ch) = *stage_at(stage, row, lane & 3);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+}
+// Short tile: a thread is channel ch, columns are rows of A.
+template <typename OutT>
+__device__ __forceinline__ void short_plain(const KP& p, const Item& it, uint32_t tb, int h, int ch, size_t gsb, OutT* out) {
+    const int lane = threadIdx.x & 31;
+    const float f = ch < p.N ? p.sb0[gsb + ch] : 0.f;
+    const float* sap = p.sa + it.row0;
+#pragma unroll 1
+    for (int c = 32 * h; c < it.n; c += 64) {
+        const float sa_c = c + lane < it.n ? sap[c + lane] : 0.f;   // lane l: the scale of row c + l
+        uint32_t v[32];
+        tmem_ld32(tb + c, v);
+        OutT* o = out + (it.row0 + c) * p.N + ch;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float y = scaled(v[j], __shfl_sync(0xffffffffu, sa_c, j), f);
+            if (c + j < it.n && ch < p.N) put(o + static_cast<size_t>(j) * p.N, y);
+        }
+    }
+}
+template <typename OutT>
+__device__ __forceinline__ void short_swiglu(const KP& p, const Item& it, uint32_t tb, int h, bool gate, int pid, float* xp,
+                                             int ch, size_t gsb, OutT* out) {
+    const int lane = threadIdx.x & 31;
+    const float f = ch < p.N ? (gate ? p.sb0 : p.sb1)[gsb + ch] : 0.f;
+    const float* sap = p.sa + it.row0;
+    float* mine = xp + (gate ? 0 : 512);
+    const float* other = xp + (gate ? 512 : 0);
+#pragma unroll 1
+    for (int c = 32 * h; c < it.n; c += 64) {
+        const float sa_c = c + lane < it.n ? sap[c + lane] : 0.f;
+        uint32_t v[32];
+        tmem_ld32(tb + c, v);
+        float keep[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {   // rows 0..15 are the gate warp's to finish, 16..31 the up warp's
+            const float lo = scaled(v[j], __shfl_sync(0xffffffffu, sa_c, j), f);
+            const float hi = scaled(v[16 + j], __shfl_sync(0xffffffffu, sa_c, 16 + j), f);
+            keep[j] = gate ? lo : hi;
+            mine[j * 32 + lane] = gate ? hi : lo;
+        }
+        pair_sync(pid);
+        const int c0 = c + (gate ? 0 : 16);
+        OutT* o = out + (it.row0 + c0) * p.N + ch;
+        float got[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) got[j] = other[j * 32 + lane];
+        pair_sync(pid);   // both have read: the buffers are free
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float a = gate ? keep[j] : got[j], b = gate ? got[j] : keep[j];
+            if (c0 + j < it.n && ch < p.N) put(o + static_cast<size_t>(j) * p.N, swiglu(a, b, out));
+        }
+    }
 }
 
 template <bool SWIGLU, typename OutT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
 i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-               const __grid_constant__ CUtensorMap tmB1, const KP p) {
+               const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmA32, const KP p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* xch = reinterpret_cast<float*>(smem + P_STAGES * P_STAGE_BYTES);
     using C = Ctl<P_STAGES>;
-    C* ctl = reinterpret_cast<C*>(smem + P_STAGES * P_STAGE_BYTES);
+    C* ctl = reinterpret_cast<C*>(xch + P_XCH_FLOATS + P_SCALE_FLOATS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     const bool leader = rank == 0;
     const uint32_t peer_abort = mapa_shared(smem_u32(&ctl->abort_flag), rank ^ 1u);
     const int cluster = static_cast<int>(blockIdx.x >> 1), nclusters = static_cast<int>(gridDim.x >> 1);
-    constexpr int TM = 256;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < P_STAGES; ++s) {
@@ -276,7 +448,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&ctl->tfull[a], 1);
-            mbar_init(&ctl->tempty[a], 8);
+            mbar_init(&ctl->tempty[a], 16);
         }
         mbar_init(&ctl->drain, 1);
         ctl->abort_flag = 0;
@@ -288,7 +460,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                      ::"r"(smem_u32(&ctl->tmem_base)), "r"(TMEM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    if (warp == 2) list_tiles(ctl, p, TM);
+    if (warp == 2) list_tiles(ctl, p, 256);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -296,29 +468,48 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const uint32_t tmem_base = ctl->tmem_base;
     const Work work = work_of(ctl->cum[p.E], nclusters);
     const int num_kb = (p.K + BKB - 1) / BKB;
+    constexpr int SET = SWIGLU ? 128 : 256;   // channels of one of a tile's two sets
+    auto sets_of = [&](const Item& it) { return it.t.n_blk * 2 * SET + SET < p.N ? 2 : 1; };
 
     if (warp == 0) {
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0, armed = 0, armed_ph = 0;
             bool aborted = false;
-            const CUtensorMap* mb = SWIGLU && rank ? &tmB1 : &tmB0;
             auto full_of = [&](int st) { return mapa_shared(smem_u32(&ctl->full[st]), 0u); };
             for (int u = cluster; u < work.items && !aborted; u += nclusters) {
-                int hf;
-                const Tile t = tile_of(ctl, p, item_tile(work, u, hf), TM);
-                const int arow = t.row0 + t.m_blk * TM + rank * BM;
-                const int brow = t.g * p.N + (SWIGLU ? t.n_blk * 128 : t.n_blk * 256 + rank * 128);
+                const Item it = item_at(ctl, p, work, u);
+                if (it.n == 0) continue;
+                const int sets = sets_of(it);
+                // this rank's rows of A: 128 in one box, or of a short tile half of its N columns in boxes of 32
+                const int half_n = (it.n + 31) / 32 * 16;
+                const int arow = static_cast<int>(it.row0) + rank * (it.shrt ? half_n : BM);
+                const int boxes = it.shrt ? (half_n + 31) / 32 : 0;
+                // its two 64-row boxes of weights of each set
+                const int b0 = it.t.g * p.N + it.t.n_blk * 2 * SET + (SWIGLU ? (it.shrt ? rank * 64 : 0) : rank * 128);
+                const int b1 = SWIGLU && it.shrt ? b0 : b0 + 64;
+                const CUtensorMap* m0 = SWIGLU && !it.shrt && rank ? &tmB1 : &tmB0;
+                const CUtensorMap* m1 = SWIGLU && it.shrt ? &tmB1 : m0;
+                const uint32_t bytes = (it.shrt ? boxes * 32 * BKB : A_BYTES) + sets * BH_BYTES;
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (!wait_i8(&ctl->empty[s], ph ^ 1u, ctl, p, peer_abort)) { aborted = true; break; }
                     const uint32_t sa = smem_u32(smem + s * P_STAGE_BYTES);
                     if (leader) {
-                        mbar_arrive_expect_tx(&ctl->full[s], 2 * P_STAGE_BYTES);
+                        mbar_arrive_expect_tx(&ctl->full[s], 2 * bytes);
                         armed |= 1u << s;
                         armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
                     }
-                    tma_load_2d_pair(sa, &tmA, full_of(s), kb * BKB, arow);
-                    tma_load_2d_pair(sa + A_BYTES, mb, full_of(s), kb * BKB, brow);
+                    if (it.shrt) {
+                        for (int q = 0; q < boxes; ++q)
+                            tma_load_2d_pair(sa + q * 32 * BKB, &tmA32, full_of(s), kb * BKB, arow + 32 * q);
+                    } else {
+                        tma_load_2d_pair(sa, &tmA, full_of(s), kb * BKB, arow);
+                    }
+                    for (int z = 0; z < sets; ++z) {
+                        const uint32_t sw = sa + A_BYTES + z * BH_BYTES;
+                        tma_load_2d_pair(sw, m0, full_of(s), kb * BKB, b0 + z * SET);
+                        tma_load_2d_pair(sw + BH_BYTES / 2, m1, full_of(s), kb * BKB, b1 + z * SET);
+                    }
                     if (++s == P_STAGES) { s = 0; ph ^= 1u; }
                 }
             }
@@ -335,33 +526,63 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
     } else if (warp == 1) {
         if (lane == 0 && leader) {
-            int s = 0, acc = 0;
-            uint32_t ph = 0, aph = 0;
+            int s = 0;
+            uint32_t ph = 0, aph[2] = {0u, 0u};
             bool aborted = false, issued = false;
             for (int u = cluster; u < work.items && !aborted; u += nclusters) {
-                int hf;
-                item_tile(work, u, hf);
-                const uint32_t id = hf < 0 ? idesc_i8(TM, 256) : idesc_i8(TM, 128);
-                const uint32_t boff = hf > 0 ? 64u * BKB : 0u;
-                if (!wait_i8(&ctl->tempty[acc], aph ^ 1u, ctl, p, peer_abort)) { aborted = true; break; }
-                tc_fence_after();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * ACC_COLS);
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!wait_i8(&ctl->full[s], ph, ctl, p, peer_abort)) { aborted = true; break; }
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + s * P_STAGE_BYTES);
-                    const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + A_BYTES + boff);
+                const Item it = item_at(ctl, p, work, u);
+                if (it.n == 0) continue;
+                const int sets = sets_of(it);
+                const uint32_t id = idesc_i8(256, it.shrt ? (it.n + 31) / 32 * 32 : 256);
+                // the K blocks [kb, kb + cnt) of set z; the last set of an item releases the stages
+                auto run = [&](int kb, int cnt, int z, int st, uint32_t p0) {
+                    for (int i = 0; i < cnt; ++i) {
+                        if (z == 0 && !wait_i8(&ctl->full[st], p0, ctl, p, peer_abort)) return false;
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + st * P_STAGE_BYTES);
+                        const uint64_t xd = sw128_desc(sa), wd = sw128_desc(sa + A_BYTES + z * BH_BYTES);
+                        const uint64_t md = it.shrt ? wd : xd, nd = it.shrt ? xd : wd;
+                        const uint32_t d = tmem_base + static_cast<uint32_t>(z * ACC_COLS);
 #pragma unroll
-                    for (int kk = 0; kk < BKB / 32; ++kk)
-                        mma_i8_pair(d, ad + 2u * kk, bd + 2u * kk, id, (kb | kk) != 0 ? 1u : 0u);
-                    issued = true;
-                    tc_commit_pair_mc(&ctl->empty[s], 0x3);
-                    if (++s == P_STAGES) { s = 0; ph ^= 1u; }
+                        for (int kk = 0; kk < BKB / 32; ++kk)
+                            mma_i8_pair(d, md + 2u * kk, nd + 2u * kk, id, (kb + i) | kk ? 1u : 0u);
+                        issued = true;
+                        if (z == sets - 1) tc_commit_pair_mc(&ctl->empty[st], 0x3);
+                        if (++st == P_STAGES) { st = 0; p0 ^= 1u; }
+                    }
+                    return true;
+                };
+                auto step = [&](int cnt) {
+                    s += cnt;
+                    if (s >= P_STAGES) { s -= P_STAGES; ph ^= 1u; }
+                };
+                auto free_acc = [&](int z) {
+                    const bool ok = wait_i8(&ctl->tempty[z], aph[z] ^ 1u, ctl, p, peer_abort);
+                    aph[z] ^= 1u;
+                    tc_fence_after();
+                    return ok;
+                };
+                // With two sets the first and last P_STAGES K blocks go set by set: set 0
+                // starts while the epilogue still reads set 1 of the tile before, and is
+                // complete while set 1 still runs.
+                const int first = min(P_STAGES, num_kb), last = sets == 2 ? min(P_STAGES, num_kb - first) : 0;
+                bool ok = free_acc(0) && run(0, first, 0, s, ph);
+                if (ok && first == num_kb) tc_commit_pair_mc(&ctl->tfull[0], 0x3);
+                if (ok && sets == 2) ok = free_acc(1) && run(0, first, 1, s, ph);
+                if (ok) step(first);
+                for (int kb = first; ok && kb < num_kb - last; ++kb) {
+                    ok = run(kb, 1, 0, s, ph);
+                    if (ok && sets == 2) ok = run(kb, 1, 1, s, ph);
+                    if (ok) step(1);
                 }
-                if (aborted) break;
-                tc_commit_pair_mc(&ctl->tfull[acc], 0x3);
-                acc ^= 1;
-                if (acc == 0) aph ^= 1u;
+                if (ok && first < num_kb) {
+                    ok = run(num_kb - last, last, 0, s, ph);
+                    if (ok) tc_commit_pair_mc(&ctl->tfull[0], 0x3);
+                    if (ok && sets == 2) ok = run(num_kb - last, last, 1, s, ph);
+                    if (ok) step(last);
+                }
+                if (ok && sets == 2) tc_commit_pair_mc(&ctl->tfull[1], 0x3);
+                aborted = !ok;
             }
             if (aborted && issued) {
                 tc_commit_pair(&ctl->drain);
@@ -370,38 +591,53 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
     } else {
         const int q = warp & 3;
-        const int r = rank * BM + q * 32 + lane;
-        const uint32_t tempty0[2] = {mapa_shared(smem_u32(&ctl->tempty[0]), 0u),
-                                     mapa_shared(smem_u32(&ctl->tempty[1]), 0u)};
-        int acc = 0;
-        uint32_t aph = 0;
-        for (int u = cluster; u < work.items; u += nclusters) {
-            int hf;
-            const Tile t = tile_of(ctl, p, item_tile(work, u, hf), TM);
-            const int grow = t.m_blk * TM + r;
-            const bool valid = grow < t.rows;
-            const size_t orow = static_cast<size_t>(t.row0) + static_cast<size_t>(grow);
-            const float sa = valid ? p.sa[orow] : 0.f;
-            if (!wait_i8(&ctl->tfull[acc], aph, ctl, p, peer_abort)) break;
-            tc_fence_after();
-            const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * ACC_COLS);
-            if (hf < 0) {
-                if (SWIGLU) store_cols<true, OutT>(p, tb, 128, 128, t.n_blk * 128, t.g, valid, orow, sa);
-                else store_cols<false, OutT>(p, tb, 0, 256, t.n_blk * 256, t.g, valid, orow, sa);
-            } else if (SWIGLU) {
-                store_cols<true, OutT>(p, tb, 64, 64, t.n_blk * 128 + 64 * hf, t.g, valid, orow, sa);
-            } else {
-                store_cols<false, OutT>(p, tb, 0, 64, t.n_blk * 256 + 64 * hf, t.g, valid, orow, sa);
-                store_cols<false, OutT>(p, tb + 64, 0, 64, t.n_blk * 256 + 128 + 64 * hf, t.g, valid, orow, sa);
+        const bool gate = q < 2;                      // short SWIGLU tiles: this warp's accumulators
+        const int h = (warp - 2) >> 2;                // which half of a set's columns
+        const int pid = 1 + (q & 1) + 2 * h;          // barrier of the warp pair
+        float* xp = xch + (pid - 1) * 2 * 512;
+        float* scales = xch + P_XCH_FLOATS + (warp - 2) * 128;
+        // whole tiles stage in the 2 KB in which the warp sends its half of a short one (read by the partner before
+        // the barrier that ends every trade)
+        uint8_t* stage = reinterpret_cast<uint8_t*>(xp + (gate ? 0 : 512));
+        uint32_t tempty0[2] = {mapa_shared(smem_u32(&ctl->tempty[0]), 0u), mapa_shared(smem_u32(&ctl->tempty[1]), 0u)};
+        OutT* out = static_cast<OutT*>(p.out);
+        uint32_t aph[2] = {0u, 0u};
+        bool alive = true;
+        for (int u = cluster; u < work.items && alive; u += nclusters) {
+            const Item it = item_at(ctl, p, work, u);
+            if (it.n == 0) continue;
+            const int sets = sets_of(it);
+            const size_t gsb = static_cast<size_t>(it.t.g) * p.N;
+            for (int z = 0; z < sets; ++z) {
+                const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(z * ACC_COLS);
+                const int ch0 = it.t.n_blk * 2 * SET + z * SET;
+                // the scales of the epilogue are fetched before its wait
+                const int r = rank * BM + q * 32 + lane;
+                const float sa = !it.shrt && r < it.n ? p.sa[it.row0 + r] : 0.f;
+                if (!it.shrt) {
+                    __syncwarp();   // the warp has read the ones before
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const int ch = ch0 + (SWIGLU ? 64 * h + 32 * (v & 1) : 128 * h + 32 * v) + lane;
+                        scales[32 * v + lane] = ch < p.N ? (SWIGLU && v >= 2 ? p.sb1 : p.sb0)[gsb + ch] : 0.f;
+                    }
+                    __syncwarp();
+                }
+                const bool ok = wait_i8(&ctl->tfull[z], aph[z], ctl, p, peer_abort);
+                aph[z] ^= 1u;
+                // the warps of a pair leave together, so that neither waits for the other
+                if (SWIGLU ? !pair_and(pid, ok) : !ok) { alive = false; break; }
+                tc_fence_after();
+                if (!it.shrt) whole_tile<SWIGLU, OutT>(p, it, tb, h, r - lane, ch0, sa, scales, stage, out);
+                else if (SWIGLU) short_swiglu<OutT>(p, it, tb, h, gate, pid, xp, ch0 + rank * 64 + (q & 1) * 32 + lane, gsb, out);
+                else short_plain<OutT>(p, it, tb, h, ch0 + rank * 128 + q * 32 + lane, gsb, out);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader) mbar_arrive(&ctl->tempty[z]);
+                    else mbar_arrive_remote(tempty0[z]);
+                }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (leader) mbar_arrive(&ctl->tempty[acc]);
-                else mbar_arrive_remote(tempty0[acc]);
-            }
-            acc ^= 1;
-            if (acc == 0) aph ^= 1u;
         }
     }
     tc_fence_before();
@@ -490,13 +726,11 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, uint32_t (
 __device__ __forceinline__ void red_add(int* p, uint32_t v) {
     asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 template <bool SWIGLU, typename OutT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-                 const __grid_constant__ CUtensorMap tmB1, const KP p) {
+                 const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap, const KP p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     using C = Ctl<S_STAGES>;
@@ -661,10 +895,9 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     for (int j = 0; j < 16; ++j) {
                         const float sa = __shfl_sync(0xffffffffu, sa_c, (c & 16) + j);
                         const bool in = c + j < nrow;
-                        const float y0 = static_cast<float>(static_cast<int>(lo[j])) * sa * f0;
-                        const float y1 = static_cast<float>(static_cast<int>(hi[j])) * sa * f1;
+                        const float y0 = scaled(lo[j], sa, f0), y1 = scaled(hi[j], sa, f1);
                         if (SWIGLU) {
-                            if (in && ch0 < p.N) put(o + static_cast<size_t>(j) * p.N + ch0, silu(y0, out) * y1);
+                            if (in && ch0 < p.N) put(o + static_cast<size_t>(j) * p.N + ch0, swiglu(y0, y1, out));
                         } else {
                             if (in && ch0 < p.N) put(o + static_cast<size_t>(j) * p.N + ch0, y0);
                             if (in && ch1 < p.N) put(o + static_cast<size_t>(j) * p.N + ch1, y1);
@@ -737,22 +970,23 @@ bool map_i8(CUtensorMap* m, const void* base, long long rows, int cols, int box_
 }
 
 template <typename Kernel>
-cudaError_t launch_tc(Kernel kernel, size_t smem, int grid, const CUtensorMap& a, const CUtensorMap& b0,
-                      const CUtensorMap& b1, const KP& kp, cudaStream_t st) {
+cudaError_t launch_tc(Kernel kernel, size_t smem, int grid, int threads, const CUtensorMap& a, const CUtensorMap& b0,
+                      const CUtensorMap& b1, const CUtensorMap& a32, const KP& kp, cudaStream_t st) {
     // the attribute belongs to the current device's context: set at every launch (a host-side call of about 1 us)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_k(kernel, dim3(grid), dim3(NUM_THREADS), smem, st, a, b0, b1, kp);
+    return launch_k(kernel, dim3(grid), dim3(threads), smem, st, a, b0, b1, a32, kp);
 }
 
 template <bool SWIGLU, typename OutT>
 cudaError_t launch_form(const I8Gemm& g, const KP& kp, const CUtensorMap& a, const CUtensorMap& b0,
-                        const CUtensorMap& b1, cudaStream_t st) {
+                        const CUtensorMap& b1, const CUtensorMap& a32, cudaStream_t st) {
     if (g.form == I8_PAIR)
-        return launch_tc(i8_pair_kernel<SWIGLU, OutT>, P_STAGES * P_STAGE_BYTES + 1024 + sizeof(Ctl<P_STAGES>),
-                         device_sm_count() & ~1, a, b0, b1, kp, st);
+        return launch_tc(i8_pair_kernel<SWIGLU, OutT>,
+                         P_STAGES * P_STAGE_BYTES + (P_XCH_FLOATS + P_SCALE_FLOATS) * 4 + 1024 + sizeof(Ctl<P_STAGES>),
+                         device_sm_count() & ~1, P_THREADS, a, b0, b1, a32, kp, st);
     return launch_tc(i8_single_kernel<SWIGLU, OutT>, S_STAGES * S_STAGE_BYTES + 1024 + sizeof(Ctl<S_STAGES>),
-                     std::min(device_sm_count(), kI8MaxGrid), a, b0, b1, kp, st);
+                     std::min(device_sm_count(), kI8MaxGrid), NUM_THREADS, a, b0, b1, a32, kp, st);
 }
 
 }  // namespace
@@ -760,16 +994,19 @@ cudaError_t launch_form(const I8Gemm& g, const KP& kp, const CUtensorMap& a, con
 cudaError_t launch_i8_tc(const I8Gemm& g, cudaStream_t st) {
     const bool swiglu = g.B1 != nullptr, pair = g.form == I8_PAIR;
     const long long brows = static_cast<long long>(g.E) * g.N;
-    CUtensorMap a, b0, b1;
-    if (!map_i8(&a, g.A, g.rows, g.K, pair ? BM : 32) || !map_i8(&b0, g.B0, brows, g.K, 128)) return cudaErrorInvalidValue;
+    CUtensorMap a, b0, b1, a32;
+    const int bbox = pair ? 64 : 128;
+    if (!map_i8(&a, g.A, g.rows, g.K, pair ? BM : 32) || !map_i8(&b0, g.B0, brows, g.K, bbox)) return cudaErrorInvalidValue;
     b1 = b0;
-    if (swiglu && !map_i8(&b1, g.B1, brows, g.K, 128)) return cudaErrorInvalidValue;
+    a32 = a;
+    if (pair && !map_i8(&a32, g.A, g.rows, g.K, 32)) return cudaErrorInvalidValue;
+    if (swiglu && !map_i8(&b1, g.B1, brows, g.K, bbox)) return cudaErrorInvalidValue;
     KP kp = {};
     kp.indptr = g.indptr; kp.sa = g.sa; kp.sb0 = g.sb0; kp.sb1 = g.sb1; kp.out = g.out; kp.status = g.status;
     kp.timeout_ns = wait_limit_ns();
     kp.drain_ns = kDrainLimitNs;
     kp.E = g.E; kp.N = g.N; kp.K = g.K; kp.rows = g.rows;
-    kp.nt = ceil_div(g.N, swiglu ? 128 : 256);
+    kp.nt = ceil_div(g.N, (swiglu ? 128 : 256) * (pair ? 2 : 1));
     const long long blk = static_cast<long long>(pair ? 256 : BM) * g.K;
     kp.band_m = static_cast<int>(std::max(8ll, kBandBytes / blk));
     if (!pair) { kp.part = g.part; kp.sem = g.sem; kp.part_rows = g.part_rows; }
@@ -782,9 +1019,9 @@ cudaError_t launch_i8_tc(const I8Gemm& g, cudaStream_t st) {
         ~Dependent() { g_pdl = false; }
     } dependent;
     if (g.out_dtype == MOE_DTYPE_BF16)
-        return swiglu ? launch_form<true, __nv_bfloat16>(g, kp, a, b0, b1, st)
-                      : launch_form<false, __nv_bfloat16>(g, kp, a, b0, b1, st);
-    return swiglu ? launch_form<true, float>(g, kp, a, b0, b1, st) : launch_form<false, float>(g, kp, a, b0, b1, st);
+        return swiglu ? launch_form<true, __nv_bfloat16>(g, kp, a, b0, b1, a32, st)
+                      : launch_form<false, __nv_bfloat16>(g, kp, a, b0, b1, a32, st);
+    return swiglu ? launch_form<true, float>(g, kp, a, b0, b1, a32, st) : launch_form<false, float>(g, kp, a, b0, b1, a32, st);
 }
 
 }  // namespace moe
