@@ -344,6 +344,17 @@ int moe_quantize_rows(int32_t dtype, const void* x, int32_t rows, int32_t cols, 
  * initialisation), 0 when p is not one they take. */
 size_t moe_int8_workspace_size(const moe_problem* p);
 
+/* Which form a product of p takes (down = 0: up, else down):
+ * MOE_INT8_PAIR (CTA pairs, tiles of 256 rows x 512 weight rows) where the
+ * experts average at least 256 rows and the tiles fill the GPU,
+ * MOE_INT8_SINGLE (single CTAs, the weights as the M operand, the last tiles
+ * cut along K) otherwise. The sums are exact and the scales applied alike: the
+ * results are the same bits. A negative MOE_ERR_* code if p is not one they
+ * take. Host only. */
+#define MOE_INT8_SINGLE 0
+#define MOE_INT8_PAIR   1
+int moe_int8_variant(const moe_problem* p, int down);
+
 /* moe_permute with the rows in 8 bits: pos, indptr, row_token and stats as
  * there (row_token is required); xq [Rmax, d] and xs [Rmax] hold the
  * quantised row of the token of each permuted row (each token is quantised

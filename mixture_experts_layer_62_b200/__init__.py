@@ -117,6 +117,8 @@ def _load():
     lib.moe_quantize_rows.restype = ctypes.c_int
     lib.moe_int8_workspace_size.argtypes = [P]
     lib.moe_int8_workspace_size.restype = sz
+    lib.moe_int8_variant.argtypes = [P, ctypes.c_int]
+    lib.moe_int8_variant.restype = ctypes.c_int
     lib.moe_permute_int8.argtypes = [P] + [vp] * 8 + [vp, sz, vp]
     lib.moe_permute_int8.restype = ctypes.c_int
     lib.moe_expert_up_int8.argtypes = [P] + [vp] * 9 + [vp, sz, vp]
@@ -363,6 +365,49 @@ def permute_noalloc(p: Problem, x, idx, pos, indptr, row_token, xp, stats, strea
     _check(rc, "moe_permute_noalloc")
 
 
+# The calls below are short next to a decode step, so their arguments are
+# marshalled without objects in between: plain integers for pointers and the
+# stream, and one look at each tensor.
+
+def _device(t) -> int:
+    """The current device, which the tensors of a call have to be on."""
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the MoE library must be CUDA tensors")
+    return torch._C._cuda_getDevice()
+
+
+def _at(t, dev):
+    """Address of a tensor of the current device (None: NULL)."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"tensors passed to the MoE library must be CUDA tensors of the current device (cuda:{dev}), "
+                         f"got one on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the MoE library must be contiguous")
+    return t.data_ptr()
+
+
+def _on(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _typed(t, dtype, numel, name):
+    """A tensor of another type or too small would be read as something else, or past its end."""
+    if t.dtype is not dtype or t.numel() < numel:
+        raise ValueError(f"{name}: expected {dtype} with at least {numel} elements, got {t.dtype} with {t.numel()}")
+
+
+def _rows(p: Problem) -> int:
+    """permuted_rows without the call (p is checked by the library)."""
+    return p.T * p.k + (p.E * (p.pad_rows - 1) if p.pad_rows > 0 else 0)
+
+
+_I8, _I32, _F32 = torch.int8, torch.int32, torch.float32
+
+
 # ---- experts in 8-bit integers ------------------------------------------------
 
 def int8_workspace_size(p: Problem) -> int:
@@ -376,6 +421,17 @@ def alloc_int8_workspace(p: Problem, device=None) -> torch.Tensor:
     return torch.empty(int8_workspace_size(p), dtype=torch.uint8, device=device or "cuda")
 
 
+INT8_VARIANTS = {0: "single", 1: "pair"}
+
+
+def int8_variant(p: Problem, down: bool = False) -> str:
+    """Name of the kernel form that the up (or down) product of p takes in 8 bits (moe_int8_variant)."""
+    v = int(_lib().moe_int8_variant(ctypes.byref(p), 1 if down else 0))
+    if v < 0:
+        raise MoEError(-v, "moe_int8_variant")
+    return INT8_VARIANTS[v]
+
+
 def quantize_rows(x, q=None, scale=None, used=None, stream=None):
     """Rows of x [..., cols] in 8 bits with a scale for each row (see
     moe_quantize_rows); used: a one-element int32 tensor, the rows to take.
@@ -383,66 +439,103 @@ def quantize_rows(x, q=None, scale=None, used=None, stream=None):
     cols = x.shape[-1]
     rows = x.numel() // cols if cols else 0
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        q = torch.empty(x.shape, dtype=_I8, device=x.device)
     if scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    _typed(q, torch.int8, rows * cols, "q")
-    _typed(scale, torch.float32, rows, "scale")
+        scale = torch.empty(x.shape[:-1], dtype=_F32, device=x.device)
+    _typed(q, _I8, rows * cols, "q")
+    _typed(scale, _F32, rows, "scale")
     if used is not None:
-        _typed(used, torch.int32, 1, "used")
-    rc = _lib().moe_quantize_rows(_dtype_code(x.dtype), _ptr(x), rows, cols, _ptr(used), _ptr(q), _ptr(scale),
-                                  _stream(stream))
-    _check(rc, "moe_quantize_rows")
+        _typed(used, _I32, 1, "used")
+    code = _dtype_code(x.dtype)
+    dev = _device(x)
+    rc = _lib().moe_quantize_rows(code, _at(x, dev), rows, cols, _at(used, dev), _at(q, dev), _at(scale, dev),
+                                  _on(stream, dev))
+    if rc:
+        raise MoEError(rc, "moe_quantize_rows")
     return q, scale
 
 
 def permute_int8(p: Problem, x, idx, pos, indptr, row_token, xq, xs, stats, workspace, stream=None):
     """moe_permute with the token rows in 8 bits (see moe_permute_int8)."""
-    _typed(xq, torch.int8, permuted_rows(p) * p.d, "xq")
-    _typed(xs, torch.float32, permuted_rows(p), "xs")
-    rc = _lib().moe_permute_int8(ctypes.byref(p), _ptr(x), _ptr(idx), _ptr(pos), _ptr(indptr), _ptr(row_token),
-                                 _ptr(xq), _ptr(xs), _ptr(stats), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(rc, "moe_permute_int8")
+    rows, pairs = _rows(p), p.T * p.k
+    _typed(x, torch_dtype(p.dtype), p.T * p.d, "x")
+    _typed(idx, _I32, pairs, "idx")
+    _typed(pos, _I32, pairs, "pos")
+    _typed(indptr, _I32, p.E + 1, "indptr")
+    _typed(row_token, _I32, rows, "row_token")
+    _typed(xq, _I8, rows * p.d, "xq")
+    _typed(xs, _F32, rows, "xs")
+    _typed(stats, torch.uint8, STATS_HEADER_BYTES + 16 * p.E, "stats")
+    dev = _device(x)
+    rc = _lib().moe_permute_int8(ctypes.byref(p), _at(x, dev), _at(idx, dev), _at(pos, dev), _at(indptr, dev),
+                                 _at(row_token, dev), _at(xq, dev), _at(xs, dev), _at(stats, dev), _at(workspace, dev),
+                                 workspace.nbytes, _on(stream, dev))
+    if rc:
+        raise MoEError(rc, "moe_permute_int8")
 
 
 def expert_up_int8(p: Problem, xq, xs, indptr, W1, w1s, W3, w3s, h, workspace, stats=None, stream=None):
     """h = SiLU(a) b over 8-bit rows and weights with their scales; see moe_expert_up_int8."""
-    _typed(xq, torch.int8, permuted_rows(p) * p.d, "xq")
-    _typed(W1, torch.int8, p.E * p.d_ff * p.d, "W1")
-    _typed(W3, torch.int8, p.E * p.d_ff * p.d, "W3")
-    rc = _lib().moe_expert_up_int8(ctypes.byref(p), _ptr(xq), _ptr(xs), _ptr(indptr), _ptr(W1), _ptr(w1s), _ptr(W3),
-                                   _ptr(w3s), _ptr(h), _ptr(stats), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(rc, "moe_expert_up_int8")
+    rows, E, d, dff = _rows(p), p.E, p.d, p.d_ff
+    _typed(xq, _I8, rows * d, "xq")
+    _typed(xs, _F32, rows, "xs")
+    _typed(indptr, _I32, E + 1, "indptr")
+    _typed(W1, _I8, E * dff * d, "W1")
+    _typed(w1s, _F32, E * dff, "w1s")
+    _typed(W3, _I8, E * dff * d, "W3")
+    _typed(w3s, _F32, E * dff, "w3s")
+    _typed(h, torch_dtype(p.dtype), rows * dff, "h")
+    dev = _device(xq)
+    rc = _lib().moe_expert_up_int8(ctypes.byref(p), _at(xq, dev), _at(xs, dev), _at(indptr, dev), _at(W1, dev),
+                                   _at(w1s, dev), _at(W3, dev), _at(w3s, dev), _at(h, dev), _at(stats, dev),
+                                   _at(workspace, dev), workspace.nbytes, _on(stream, dev))
+    if rc:
+        raise MoEError(rc, "moe_expert_up_int8")
 
 
 def expert_down_int8(p: Problem, hq, hs, indptr, W2, w2s, o, workspace, stats=None, stream=None):
     """o = hq W2^T over 8-bit rows and weights with their scales; see moe_expert_down_int8."""
-    _typed(hq, torch.int8, permuted_rows(p) * p.d_ff, "hq")
-    _typed(W2, torch.int8, p.E * p.d * p.d_ff, "W2")
-    rc = _lib().moe_expert_down_int8(ctypes.byref(p), _ptr(hq), _ptr(hs), _ptr(indptr), _ptr(W2), _ptr(w2s), _ptr(o),
-                                     _ptr(stats), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                     _stream(stream))
-    _check(rc, "moe_expert_down_int8")
-
-
-def _typed(t, dtype, numel, name):
-    """A tensor of another type or too small would be read as something else, or past its end."""
-    if t.dtype != dtype or t.numel() < numel:
-        raise ValueError(f"{name}: expected {dtype} with at least {numel} elements, got {t.dtype} with {t.numel()}")
+    rows, E, d, dff = _rows(p), p.E, p.d, p.d_ff
+    _typed(hq, _I8, rows * dff, "hq")
+    _typed(hs, _F32, rows, "hs")
+    _typed(indptr, _I32, E + 1, "indptr")
+    _typed(W2, _I8, E * d * dff, "W2")
+    _typed(w2s, _F32, E * d, "w2s")
+    _typed(o, torch_dtype(p.dtype), rows * d, "o")
+    dev = _device(hq)
+    rc = _lib().moe_expert_down_int8(ctypes.byref(p), _at(hq, dev), _at(hs, dev), _at(indptr, dev), _at(W2, dev),
+                                     _at(w2s, dev), _at(o, dev), _at(stats, dev), _at(workspace, dev),
+                                     workspace.nbytes, _on(stream, dev))
+    if rc:
+        raise MoEError(rc, "moe_expert_down_int8")
 
 
 # ---- the way back, with dropout, residual and gradients -------------------------
 
+def _rng(rng):
+    if rng is not None and (rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2):
+        raise ValueError("rng: expected two 64-bit integers (seed, offset)")
+    return rng
+
+
 def combine_dropout(p: Problem, o, pos, gate, out, s=None, residual=None, prob=0.0, rng=None, stream=None):
     """out_t = residual_t + dropout(sum_j gate[t,j] o[pos[t,j]] (+ s_t)); rng: a
     device tensor of two 64-bit integers (seed, offset). See moe_combine_dropout."""
-    if rng is not None:
-        _rng(rng)
-    rc = _lib().moe_combine_dropout(ctypes.byref(p), _ptr(o), _ptr(pos), _ptr(gate), _ptr(s), _ptr(residual),
-                                    float(prob), _ptr(rng), _ptr(out), _stream(stream))
-    _check(rc, "moe_combine_dropout")
+    dt, row, n = torch_dtype(p.dtype), _rows(p) * p.d, p.T * p.d
+    _typed(o, dt, row, "o")
+    _typed(pos, _I32, p.T * p.k, "pos")
+    _typed(gate, _F32, p.T * p.k, "gate")
+    _typed(out, dt, n, "out")
+    if s is not None:
+        _typed(s, dt, n, "s")
+    if residual is not None:
+        _typed(residual, dt, n, "residual")
+    _rng(rng)
+    dev = _device(o)
+    rc = _lib().moe_combine_dropout(ctypes.byref(p), _at(o, dev), _at(pos, dev), _at(gate, dev), _at(s, dev),
+                                    _at(residual, dev), prob, _at(rng, dev), _at(out, dev), _on(stream, dev))
+    if rc:
+        raise MoEError(rc, "moe_combine_dropout")
     return out
 
 
@@ -451,23 +544,38 @@ def combine_backward(p: Problem, dy, o, pos, gate, dO, dgate, ds=None, prob=0.0,
     """Gradients of combine_dropout with the same prob and rng values:
     dO[pos] = gate u, dgate = <u, o[pos]>, ds = u with u = dropout(dy); indptr
     and row_token are needed with p.pad_rows > 0. See moe_combine_backward."""
-    if rng is not None:
-        _rng(rng)
-    rc = _lib().moe_combine_backward(ctypes.byref(p), _ptr(dy), _ptr(o), _ptr(pos), _ptr(gate), float(prob), _ptr(rng),
-                                     _ptr(indptr), _ptr(row_token), _ptr(dO), _ptr(dgate), _ptr(ds), _stream(stream))
-    _check(rc, "moe_combine_backward")
+    dt, row, n = torch_dtype(p.dtype), _rows(p) * p.d, p.T * p.d
+    _typed(dy, dt, n, "dy")
+    _typed(o, dt, row, "o")
+    _typed(pos, _I32, p.T * p.k, "pos")
+    _typed(gate, _F32, p.T * p.k, "gate")
+    _typed(dO, dt, row, "dO")
+    _typed(dgate, _F32, p.T * p.k, "dgate")
+    if ds is not None:
+        _typed(ds, dt, n, "ds")
+    if p.pad_rows > 0 and indptr is not None and row_token is not None:
+        _typed(indptr, _I32, p.E + 1, "indptr")
+        _typed(row_token, _I32, _rows(p), "row_token")
+    _rng(rng)
+    dev = _device(dy)
+    rc = _lib().moe_combine_backward(ctypes.byref(p), _at(dy, dev), _at(o, dev), _at(pos, dev), _at(gate, dev), prob,
+                                     _at(rng, dev), _at(indptr, dev), _at(row_token, dev), _at(dO, dev),
+                                     _at(dgate, dev), _at(ds, dev), _on(stream, dev))
+    if rc:
+        raise MoEError(rc, "moe_combine_backward")
 
 
 def permute_backward(p: Problem, dxp, pos, dx, stream=None):
     """dx_t = sum_j dxp[pos[t,j]] over the kept pairs; see moe_permute_backward."""
-    _check(_lib().moe_permute_backward(ctypes.byref(p), _ptr(dxp), _ptr(pos), _ptr(dx), _stream(stream)),
-           "moe_permute_backward")
+    dt = torch_dtype(p.dtype)
+    _typed(dxp, dt, _rows(p) * p.d, "dxp")
+    _typed(pos, _I32, p.T * p.k, "pos")
+    _typed(dx, dt, p.T * p.d, "dx")
+    dev = _device(dxp)
+    rc = _lib().moe_permute_backward(ctypes.byref(p), _at(dxp, dev), _at(pos, dev), _at(dx, dev), _on(stream, dev))
+    if rc:
+        raise MoEError(rc, "moe_permute_backward")
     return dx
-
-
-def _rng(rng):
-    if rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2:
-        raise ValueError("rng: expected two 64-bit integers (seed, offset)")
 
 
 @dataclass

@@ -29,8 +29,20 @@ I8Layout make_i8_layout(const moe_problem& p) {
     return L;
 }
 
-I8Form i8_form(const moe_problem& p) {
-    return permuted_rows(p) >= 256LL * p.E ? I8_PAIR : I8_SINGLE;
+// CTA pairs need rows to fill their tiles of 256 x 512 (256 of SWIGLU) and
+// tiles to fill the GPU: below 256 rows an expert, or 1.5 tiles a pair of SMs
+// (with half a block an expert for its ragged end), the single form, whose
+// last tiles are cut along K, is faster. Measured, single against pair, top-2
+// of 8 experts (us): up projection 4096 -> 14336 of 1024 rows 197 / 222, of 2048
+// rows 284 / 265, of 8192 rows 904 / 712; down projection 14336 -> 4096 of 2048
+// rows (96 tiles) 134 / 154, of 3000 rows (128 tiles) 185 / 158.
+I8Form i8_form(const moe_problem& p, bool down) {
+    const long long pairs = (long long)p.T * p.k, E = p.E;
+    if (pairs < 256 * E) return I8_SINGLE;
+    const long long blocks2 = pairs / 128 + E;   // blocks of 256 rows, doubled
+    const long long cols = down ? ceil_div(p.d, 512) : ceil_div(p.d_ff, 256);
+    const int sms = device_sm_count();
+    return 2 * blocks2 * cols >= 3LL * (sms > 0 ? sms : 148) ? I8_PAIR : I8_SINGLE;
 }
 
 }  // namespace moe
@@ -87,7 +99,7 @@ int run_i8(const moe_problem* p, const int8_t* A, const float* sa, const int32_t
     g.A = A; g.sa = sa; g.B0 = B0; g.sb0 = sb0; g.B1 = B1; g.sb1 = sb1;
     g.out = out; g.out_dtype = p->dtype; g.N = N; g.K = K; g.rows = (int)permuted_rows(*p);
     g.status = stats ? static_cast<int32_t*>(stats) : reinterpret_cast<int32_t*>(ws + L.status);
-    g.form = i8_form(*p);
+    g.form = i8_form(*p, B1 == nullptr);
     g.part = reinterpret_cast<int*>(ws + L.part); g.sem = reinterpret_cast<int*>(ws + L.sem); g.part_rows = L.part_rows;
     CK(launch_i8_tc(g, static_cast<cudaStream_t>(stream)));
     return MOE_OK;
@@ -100,6 +112,12 @@ extern "C" {
 size_t moe_int8_workspace_size(const moe_problem* p) {
     if (check_int8(p) != MOE_OK) return 0;
     return make_i8_layout(*p).total;
+}
+
+int moe_int8_variant(const moe_problem* p, int down) {
+    const int rc = check_int8(p);
+    if (rc != MOE_OK) return -rc;
+    return i8_form(*p, down != 0) == I8_PAIR ? MOE_INT8_PAIR : MOE_INT8_SINGLE;
 }
 
 int moe_quantize_rows(int32_t dtype, const void* x, int32_t rows, int32_t cols, const int32_t* used, int8_t* q,

@@ -969,23 +969,28 @@ bool map_i8(CUtensorMap* m, const void* base, long long rows, int cols, int box_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename Kernel>
-cudaError_t launch_tc(Kernel kernel, size_t smem, int grid, int threads, const CUtensorMap& a, const CUtensorMap& b0,
+template <auto KERNEL>
+cudaError_t launch_tc(size_t smem, int grid, int threads, const CUtensorMap& a, const CUtensorMap& b0,
                       const CUtensorMap& b1, const CUtensorMap& a32, const KP& kp, cudaStream_t st) {
-    // the attribute belongs to the current device's context: set at every launch (a host-side call of about 1 us)
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    return launch_k(kernel, dim3(grid), dim3(threads), smem, st, a, b0, b1, a32, kp);
+    static bool attr_set[64] = {};   // per kernel (template) and device; the size never changes
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    return launch_k(KERNEL, dim3(grid), dim3(threads), smem, st, a, b0, b1, a32, kp);
 }
 
 template <bool SWIGLU, typename OutT>
 cudaError_t launch_form(const I8Gemm& g, const KP& kp, const CUtensorMap& a, const CUtensorMap& b0,
                         const CUtensorMap& b1, const CUtensorMap& a32, cudaStream_t st) {
     if (g.form == I8_PAIR)
-        return launch_tc(i8_pair_kernel<SWIGLU, OutT>,
+        return launch_tc<i8_pair_kernel<SWIGLU, OutT>>(
                          P_STAGES * P_STAGE_BYTES + (P_XCH_FLOATS + P_SCALE_FLOATS) * 4 + 1024 + sizeof(Ctl<P_STAGES>),
                          device_sm_count() & ~1, P_THREADS, a, b0, b1, a32, kp, st);
-    return launch_tc(i8_single_kernel<SWIGLU, OutT>, S_STAGES * S_STAGE_BYTES + 1024 + sizeof(Ctl<S_STAGES>),
+    return launch_tc<i8_single_kernel<SWIGLU, OutT>>(S_STAGES * S_STAGE_BYTES + 1024 + sizeof(Ctl<S_STAGES>),
                      std::min(device_sm_count(), kI8MaxGrid), NUM_THREADS, a, b0, b1, a32, kp, st);
 }
 

@@ -22,7 +22,7 @@ I8Layout make_i8_layout(const moe_problem& p);
 // One product of the experts: out[r][n] over the rows of every group.
 enum I8Form { I8_SINGLE = 0, I8_PAIR = 1 };
 constexpr int kI8MaxGrid = 160;   // CTAs of the single form at most: sizes the workspace on any host
-I8Form i8_form(const moe_problem& p);
+I8Form i8_form(const moe_problem& p, bool down);
 struct I8Gemm {
     int form;
     const int32_t* indptr;   // [E+1] (device)

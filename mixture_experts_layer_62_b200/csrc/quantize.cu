@@ -137,8 +137,8 @@ __device__ __forceinline__ uint4 quant16(const V& x, float a, float inv) {
 // thread stay in registers between the maximum and the rounding, one read of
 // the row; a longer row is read twice past that. The users walk rows with two
 // register buffers, the next row's reads running under this one's arithmetic
-// and stores: with one row a block the reads of a block had ended long before
-// it did, and 4096 rows of 4096 took 26 us in the permutation.
+// and stores: 75.5 us against 79 with a row a block (11 k rows of 14336 bf16,
+// 95 % of the copy bandwidth), 14.8 against 16.0 in the permutation of 4096 rows of 4096.
 // hold_row starts the reads, quantize_row finishes. red: TPR / 32 floats of
 // shared memory when TPR > 32, another half of it for every other row; the
 // row's threads meet at a barrier of their own. Returns scale_r; put(v, w)
