@@ -369,8 +369,11 @@ int moe_permute_int8(const moe_problem* p, const void* x, const int32_t* idx,
  *         h[r,n] = SiLU(a) b
  *   down: o[r,n] = S(hq, W2) hs[r] w2s[e,n]
  * W1, W3 [E, d_ff, d], W2 [E, d, d_ff] int8; w1s, w3s [E, d_ff], w2s [E, d]
- * fp32; h [Rmax, d_ff], o [Rmax, d] dtype, rows >= indptr[E] stay. indptr as
- * in moe_experts. stats (may be NULL): only the status word is written. */
+ * fp32 (16-byte aligned); h [Rmax, d_ff], o [Rmax, d] dtype, rows >= indptr[E]
+ * stay. indptr as in moe_experts; a group whose offsets do not fit the rows is
+ * left out (and recorded as MOE_ERR_BOUNDS by the debug build). stats (may be
+ * NULL): only the status word is written (MOE_OK, or MOE_ERR_TIMEOUT if a
+ * bounded wait gave up). */
 int moe_expert_up_int8(const moe_problem* p, const int8_t* xq, const float* xs, const int32_t* indptr,
                        const int8_t* W1, const float* w1s, const int8_t* W3, const float* w3s,
                        void* h, void* stats, void* workspace, size_t workspace_bytes, void* stream);

@@ -653,3 +653,81 @@ class MoELayer:
 
     def read_stats(self) -> Stats:
         return read_stats(self.stats, self.p.E)
+
+
+class MoELayerInt8:
+    """MoELayer with the experts in 8 bits: the same arguments, the router in
+    the problem's type, every expert weight quantised here with a scale for
+    each row (the given weights are not kept), activations quantised for each
+    token on the way. A call launches, on the current stream, moe_route,
+    moe_permute_int8, moe_expert_up_int8, moe_quantize_rows,
+    moe_expert_down_int8 and moe_combine (and for a shared expert the same
+    products with one expert over all tokens); it allocates nothing.
+
+    p.train must be 0. With ``residual`` a call returns residual + layer(x).
+    """
+
+    def __init__(self, p: Problem, W_r, W1, W3, W2, bias=None, Ws1=None, Ws3=None, Ws2=None):
+        if p.train:
+            raise MoEError(MOE_ERR_UNSUPPORTED, "MoELayerInt8")
+        self.p = p
+        self.W_r, self.bias = W_r, bias
+        dev, dt, T, d = W1.device, torch_dtype(p.dtype), p.T, p.d
+        self.experts = Problem.from_buffer_copy(p)
+        self.experts.d_ff_shared = 0
+        rows = permuted_rows(self.experts)
+        # the router's workspace holds buffers of the whole layer: a problem of the smallest hidden width
+        self.router = Problem.from_buffer_copy(self.experts)
+        self.router.d_ff = 64
+        new = lambda shape, t: torch.empty(shape, dtype=t, device=dev)  # noqa: E731
+        self.W1, self.w1s = quantize_rows(W1)
+        self.W3, self.w3s = quantize_rows(W3)
+        self.W2, self.w2s = quantize_rows(W2)
+        self.idx, self.gate, self.pos = new((T, p.k), _I32), new((T, p.k), _F32), new((T, p.k), _I32)
+        self.indptr, self.row_token = new((p.E + 1,), _I32), new((rows,), _I32)
+        self.used = self.indptr[p.E:]
+        self.xq, self.xs, self.h = new((rows, d), _I8), new((rows,), _F32), new((rows, p.d_ff), dt)
+        self.hq, self.hs, self.o = new((rows, p.d_ff), _I8), new((rows,), _F32), new((rows, d), dt)
+        self.out, self.stats = new((T, d), dt), alloc_stats(p.E, dev)
+        self.router_workspace = alloc_workspace(self.router, dev)
+        self.workspace = alloc_int8_workspace(self.experts, dev)
+        self.shared = None
+        if p.d_ff_shared:
+            f = p.d_ff_shared
+            q = problem(T, d, f, 1, 1, dtype=p.dtype)
+            self.shared = dict(p=q, W1=quantize_rows(Ws1), W3=quantize_rows(Ws3), W2=quantize_rows(Ws2),
+                               x=(new((T, d), _I8), new((T,), _F32)), h=new((T, f), dt),
+                               hq=(new((T, f), _I8), new((T,), _F32)), s=new((T, d), dt),
+                               indptr=torch.tensor([0, T], dtype=_I32, device=dev),
+                               workspace=alloc_int8_workspace(q, dev), stats=alloc_stats(1, dev))
+
+    def __call__(self, x, out=None, residual=None, stream=None):
+        out = self.out if out is None else out
+        p, s = self.experts, None
+        route(self.router, x, self.W_r, self.idx, self.gate, self.stats, self.router_workspace, bias=self.bias,
+              stream=stream)
+        permute_int8(p, x, self.idx, self.pos, self.indptr, self.row_token, self.xq, self.xs, self.stats,
+                     self.workspace, stream=stream)
+        expert_up_int8(p, self.xq, self.xs, self.indptr, self.W1, self.w1s, self.W3, self.w3s, self.h,
+                       self.workspace, stats=self.stats, stream=stream)
+        quantize_rows(self.h, self.hq, self.hs, used=self.used, stream=stream)
+        expert_down_int8(p, self.hq, self.hs, self.indptr, self.W2, self.w2s, self.o, self.workspace,
+                         stats=self.stats, stream=stream)
+        if self.shared is not None:
+            g = self.shared
+            s = g["s"]
+            quantize_rows(x, *g["x"], stream=stream)
+            expert_up_int8(g["p"], *g["x"], g["indptr"], *g["W1"], *g["W3"], g["h"], g["workspace"], stats=g["stats"],
+                           stream=stream)
+            quantize_rows(g["h"], *g["hq"], stream=stream)
+            expert_down_int8(g["p"], *g["hq"], g["indptr"], *g["W2"], s, g["workspace"], stats=g["stats"],
+                             stream=stream)
+        combine_dropout(p, self.o, self.pos, self.gate, out, s=s, residual=residual, stream=stream)
+        return out
+
+    def read_stats(self) -> Stats:
+        """The layer's statistics; the status is the last product's that did not end with MOE_OK."""
+        st = read_stats(self.stats, self.p.E)
+        if self.shared is not None and st.status == MOE_OK:
+            st.status = read_stats(self.shared["stats"], 1).status
+        return st

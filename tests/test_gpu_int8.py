@@ -264,3 +264,167 @@ def layer_inputs(T, d, dff, E, k, seed, dfs=0):
     if dfs:
         w |= dict(Ws1=n(dfs, d), Ws3=n(dfs, d), Ws2=n(d, dfs))
     return randn(g, T, d).to(torch.bfloat16), w
+
+
+LAYERS = [dict(T=1, d=256, dff=512, E=8, k=2), dict(T=40, d=512, dff=320, E=16, k=4, cf=0.9, pad=64),
+          dict(T=700, d=256, dff=448, E=4, k=2, dfs=192, bias=True), dict(T=1500, d=1024, dff=1536, E=2, k=1, cf=1.1)]
+
+
+@pytest.mark.parametrize("c", LAYERS, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
+def test_layer_stage_by_stage(c):
+    T, d, dff, E, k, dfs = c["T"], c["d"], c["dff"], c["E"], c["k"], c.get("dfs", 0)
+    x, w = layer_inputs(T, d, dff, E, k, 3, dfs)
+    bias = torch.linspace(0.4, -0.4, E, device=DEV) if c.get("bias") else None
+    p = moe.problem(T, d, dff, E, k, c.get("cf", 0.0), "bf16", bias_mode=moe.BIAS_LOGIT if c.get("bias") else 0,
+                    d_ff_shared=dfs, pad_rows=c.get("pad", 0))
+    layer = moe.MoELayerInt8(p, bias=bias, **w)
+    residual = torch.randn((T, d), device=DEV).to(torch.bfloat16)
+    y = layer(x, residual=residual)
+    st = layer.read_stats()
+    assert st.status == moe.MOE_OK
+    # the routing is moe_route's, and the statistics are whole
+    idx, gate, stats = torch.empty_like(layer.idx), torch.empty_like(layer.gate), moe.alloc_stats(E, DEV)
+    moe.route(p, x, w["W_r"], idx, gate, stats, moe.alloc_workspace(p, DEV), bias=bias)
+    assert torch.equal(idx, layer.idx) and torch.equal(gate, layer.gate)
+    ref = moe.read_stats(stats, E)
+    assert (st.counts, st.kept, st.l_aux, st.P, st.dropped) == (ref.counts, ref.kept, ref.l_aux, ref.P, ref.dropped)
+    for q, s, W in ((layer.W1, layer.w1s, w["W1"]), (layer.W2, layer.w2s, w["W2"])):
+        R.check_quantized(W.reshape(-1, W.shape[-1]), q.reshape(-1, W.shape[-1]), s.reshape(-1))
+    pos, indptr, rt, _, _ = R.permutation(idx, E, R.capacity(c.get("cf", 0.0), T, k, E), c.get("pad", 0))
+    n = int(indptr[-1])
+    rt = torch.from_numpy(rt).to(DEV)
+    assert (layer.pos.cpu().numpy() == pos).all()
+    R.check_quantized(x[rt[rt >= 0]], layer.xq[:n][rt >= 0], layer.xs[:n][rt >= 0])
+    a = R.product(layer.xq[:n], layer.xs[:n], layer.W1, layer.w1s, indptr)
+    b = R.product(layer.xq[:n], layer.xs[:n], layer.W3, layer.w3s, indptr)
+    assert ((layer.h[:n].double() - R.swiglu(a, b)).abs() <= R.swiglu_bound(a, b, torch.bfloat16)).all()
+    R.check_quantized(layer.h[:n], layer.hq[:n], layer.hs[:n])
+    o = R.product(layer.hq[:n], layer.hs[:n], layer.W2, layer.w2s, indptr)
+    assert ((layer.o[:n].double() - o).abs() <= R.plain_bound(o, torch.bfloat16)).all()
+    s = None
+    if dfs:
+        g, one = layer.shared, torch.tensor([0, T])
+        R.check_quantized(x, *g["x"])
+        a, b = (R.product(*g["x"], g[m][0][None], g[m][1][None], one) for m in ("W1", "W3"))
+        assert ((g["h"].double() - R.swiglu(a, b)).abs() <= R.swiglu_bound(a, b, torch.bfloat16)).all()
+        R.check_quantized(g["h"], *g["hq"])
+        s = R.product(*g["hq"], g["W2"][0][None], g["W2"][1][None], one)
+        assert ((g["s"].double() - s).abs() <= R.plain_bound(s, torch.bfloat16)).all()
+        s = g["s"]
+    ref, mag = R.mix(layer.o, layer.pos, layer.gate, s, residual)
+    assert ((y.double() - ref).abs() <= R.mix_bound(ref, mag, k, torch.bfloat16)).all()
+
+
+def test_layer_is_near_the_layer_in_bf16():
+    # each of the three products has two factors in 8 bits; a factor's error is
+    # at most half a step, uniform in a step of amax / 127: for normal data of
+    # these lengths amax is at most 4.5 sigma, so the relative error of one
+    # factor is at most 4.5 / (127 sqrt(12)) = 1.03 % rms. Two factors a
+    # product, and the down projection sees the up projections' through SiLU(a)
+    # b, at most 2.1 x one product's: sqrt(2 + (2.1^2) 2) x 1.03 % = 3.4 %, plus
+    # bf16's roundings. The bar is 6 %; a wrong scale or row is off by tens of
+    # percent or more.
+    T, d, dff, E, k = 300, 512, 1024, 8, 2
+    x, w = layer_inputs(T, d, dff, E, k, 9)
+    p = moe.problem(T, d, dff, E, k)
+    a, b = moe.MoELayer(p, **w)(x).double(), moe.MoELayerInt8(p, **w)(x).double()
+    assert (a - b).norm() / a.norm() < 0.06
+
+
+def test_layer_in_graphs_that_share_buffers():
+    T, d, dff, E, k = 24, 256, 512, 8, 2
+    x, w = layer_inputs(T, d, dff, E, k, 4)
+    layer = moe.MoELayerInt8(moe.problem(T, d, dff, E, k), **w)
+    outs = [torch.zeros((T, d), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    xs = [x.clone(), x.flip(0).contiguous()]
+    want = []
+    for i in range(2):
+        want.append(layer(xs[i]).clone())
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer(xs[i], out=outs[i])
+        graphs.append(g)
+    layer.workspace.fill_(0x5A)      # the workspace's contents are nobody's
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1)):
+        for o in outs:
+            o.zero_()
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in order:
+            assert torch.equal(outs[i], want[i])
+    xs[0].copy_(xs[1])               # a replay reads what the inputs hold then
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[1])
+
+
+def test_two_streams_at_once():
+    T, d, dff, E, k = 400, 512, 1024, 8, 2
+    x, w = layer_inputs(T, d, dff, E, k, 5)
+    layers = [moe.MoELayerInt8(moe.problem(T, d, dff, E, k), **w) for _ in range(2)]
+    xs = [x, (x.float() * 0.5).flip(1).to(torch.bfloat16).contiguous()]
+    want = [layers[i](xs[i]).clone() for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            layers[i].out.zero_()
+            streams[i].wait_stream(torch.cuda.current_stream())
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                layers[i](xs[i])
+        torch.cuda.synchronize()
+        assert all(torch.equal(layers[i].out, want[i]) for i in range(2))
+    # and given as an argument, from another current stream
+    layers[0].out.zero_()
+    streams[1].wait_stream(torch.cuda.current_stream())
+    layers[0](xs[0], stream=streams[1])
+    streams[1].synchronize()
+    assert torch.equal(layers[0].out, want[0])
+
+
+def test_variants_by_size():
+    v = lambda T, d, dff, E, k: (moe.int8_variant(moe.problem(T, d, dff, E, k)),  # noqa: E731
+                                 moe.int8_variant(moe.problem(T, d, dff, E, k), down=True))
+    assert v(1, 4096, 14336, 8, 2) == ("single", "single")
+    assert v(4096, 4096, 14336, 8, 2) == ("pair", "pair")
+    assert v(1024, 4096, 14336, 8, 2) == ("pair", "single")
+    assert v(2048, 7168, 2048, 256, 8) == ("single", "single")
+
+
+@pytest.mark.parametrize("T,d,dff,E,k", [(2000, 512, 4096, 2, 1), (4000, 512, 8192, 4, 1), (3000, 4096, 1088, 2, 2)])
+def test_products_in_pairs(T, d, dff, E, k):
+    # sizes whose products run on CTA pairs: whole tiles, ragged ends of every kind, empty groups
+    p = moe.problem(T, d, dff, E, k)
+    assert "pair" in (moe.int8_variant(p), moe.int8_variant(p, down=True))
+    R_ = T * k
+    for cut in ([R_], [1], [R_ - 31], [256], [R_ // 2 + 7], [0]):
+        ends = torch.tensor([0] + [min(cut[0], R_)] * (E - 1) + [R_], dtype=torch.int32)
+        run_products(T, d, dff, E, k, "bf16", ends, gen(cut[0] + 1))
+
+
+def test_products_in_pairs_f32():
+    T, d, dff, E = 1700, 1040, 4112, 2
+    p = moe.problem(T, d, dff, E, 1, 0.0, "f32")
+    assert moe.int8_variant(p) == "pair"
+    for cut in (1, 850, 1699):
+        run_products(T, d, dff, E, 1, "f32", torch.tensor([0, cut, T], dtype=torch.int32), gen(cut))
+
+
+def test_bad_offsets_are_left_out():
+    # offsets that do not fit the rows: those groups are skipped, the others run
+    T, d, E, dff = 64, 128, 4, 192
+    p = moe.problem(T, d, dff, E, 1)
+    g = gen(8)
+    q, s, W, ws_ = ints(g, T, dff), torch.rand((T,), generator=g, device=DEV), ints(g, E, d, dff), torch.ones((E, d), device=DEV)
+    o = torch.full((T, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    indptr = torch.tensor([0, 20, 70, 30, 64], dtype=torch.int32, device=DEV)   # 1 ends past the rows, 2 runs backwards
+    moe.expert_down_int8(p, q, s, indptr, W, ws_, o, moe.alloc_int8_workspace(p, DEV))
+    for e, lo, hi in ((0, 0, 20), (3, 30, 64)):
+        r = (q[lo:hi].double() @ W[e].double().T) * s[lo:hi, None].double()
+        assert ((o[lo:hi].double() - r).abs() <= R.plain_bound(r, torch.bfloat16)).all()
+    assert (o[20:30] == 7.0).all()
