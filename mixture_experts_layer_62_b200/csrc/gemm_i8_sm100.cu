@@ -113,10 +113,7 @@ __device__ __forceinline__ void list_tiles(Ctl<STAGES>* c, const KP& p, int tile
         base += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) c->cum[p.E] = base;
-    if (kDebugChecks && __any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) {
-        pdl_wait();
-        debug_record_bounds(p.status);
-    }
+    if (kDebugChecks && __any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) debug_record_bounds(p.status);
 }
 
 struct Tile {
@@ -161,7 +158,6 @@ __device__ __forceinline__ bool wait_i8(uint64_t* bar, uint32_t parity, C* ctl, 
         if (global_timer_ns() - t0 > static_cast<uint64_t>(p.timeout_ns)) {
             *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
             if (peer_abort) st_shared_remote_u32(peer_abort, 1u);
-            pdl_wait();   // the status word has been reset by then
             atomicExch(p.status, MOE_ERR_TIMEOUT);
             return false;
         }
@@ -172,7 +168,6 @@ __device__ __forceinline__ void drain_i8(uint64_t* bar, uint32_t parity, const K
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(bar, parity))
         if (global_timer_ns() - t0 > static_cast<uint64_t>(p.drain_ns)) {
-            pdl_wait();
             atomicExch(p.status, MOE_ERR_TIMEOUT);
             return;
         }
@@ -460,6 +455,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                      ::"r"(smem_u32(&ctl->tmem_base)), "r"(TMEM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    pdl_wait();
     if (warp == 2) list_tiles(ctl, p, 256);
     tc_fence_before();
     __syncthreads();
@@ -757,9 +753,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                      ::"r"(smem_u32(&ctl->tmem_base)), "r"(TMEM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // what this call's first launch writes (the status word and the arrival
-    // counters) is touched only after the wait at the epilogue's start or by
-    // a wait that gave up; all else was complete before that launch began
+    pdl_wait();
     if (warp == 2) list_tiles(ctl, p, BM);
     tc_fence_before();
     __syncthreads();
@@ -838,7 +832,6 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const int q = warp & 3, r = q * 32 + lane;   // this thread's channel of each half
         int acc = 0;
         uint32_t aph = 0;
-        pdl_wait();
         OutT* out = static_cast<OutT*>(p.out);
         Unit w;
         for (int i = 0; unit_at(un, b, i, w); ++i) {
@@ -923,12 +916,14 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 }
 
 // First launch of a product: the status word is MOE_OK, and the arrival
-// counters and accumulators of the tail tiles are zero, before any CTA of the
-// product touches them. The product starts beside it (it needs nothing of
-// this until its own wait).
+// counters and sums of the tail tiles are zero, before the product passes its
+// wait. The product's launch and prologue run beside it and the kernel
+// before; neither product triggers a next launch early, so that a following
+// call's zeros cannot meet this one's sums.
 __global__ void __launch_bounds__(256) i8_begin_kernel(const KP p, int grid) {
     __shared__ Ctl<1> c;
     pdl_launch();
+    pdl_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = MOE_OK;
     if (p.part == nullptr) return;
     if (threadIdx.x < 32) list_tiles(&c, p, BM);
@@ -980,7 +975,7 @@ cudaError_t launch_tc(size_t smem, int grid, int threads, const CUtensorMap& a, 
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    return launch_k(KERNEL, dim3(grid), dim3(threads), smem, st, a, b0, b1, a32, kp);
+    return launch_dep(KERNEL, dim3(grid), dim3(threads), smem, st, a, b0, b1, a32, kp);
 }
 
 template <bool SWIGLU, typename OutT>
@@ -1017,12 +1012,8 @@ cudaError_t launch_i8_tc(const I8Gemm& g, cudaStream_t st) {
     if (!pair) { kp.part = g.part; kp.sem = g.sem; kp.part_rows = g.part_rows; }
     const int grid = std::min(device_sm_count(), kI8MaxGrid);
     if (grid < 2) return cudaErrorInvalidDevice;
-    cudaError_t e = launch_k(i8_begin_kernel, dim3(pair ? 1 : grid), dim3(256), 0, st, kp, grid);
+    cudaError_t e = launch_dep(i8_begin_kernel, dim3(pair ? 1 : grid), dim3(256), 0, st, kp, grid);
     if (e != cudaSuccess) return e;
-    struct Dependent {   // the product is launched as a programmatic dependent of it
-        Dependent() { g_pdl = true; }
-        ~Dependent() { g_pdl = false; }
-    } dependent;
     if (g.out_dtype == MOE_DTYPE_BF16)
         return swiglu ? launch_form<true, __nv_bfloat16>(g, kp, a, b0, b1, a32, st)
                       : launch_form<false, __nv_bfloat16>(g, kp, a, b0, b1, a32, st);

@@ -7,6 +7,24 @@
 
 namespace moe {
 
+// Launch as a programmatic dependent of whatever precedes it on the stream:
+// the kernel's own launch and prologue overlap the end of the one before,
+// and it calls pdl_wait() (which returns when everything before has completed
+// and is visible) in every thread before it touches global memory, so calls
+// order as ever. Kernels launched this way call pdl_launch() early for the
+// next one, except where two calls could share a workspace.
+struct DependentLaunch {
+    DependentLaunch() : was(g_pdl) { g_pdl = true; }
+    ~DependentLaunch() { g_pdl = was; }
+    bool was;
+};
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_dep(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                              Args&&... args) {
+    DependentLaunch dependent;
+    return launch_k(kernel, grid, block, smem, st, std::forward<Args>(args)...);
+}
+
 // ---- 8-bit experts ----------------------------------------------------------
 
 // Byte offsets of moe_int8_workspace_size(p) bytes.

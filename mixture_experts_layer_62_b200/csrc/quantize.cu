@@ -212,6 +212,8 @@ quantize_kernel(const T* __restrict__ x, int rows, int cols, const int32_t* __re
     constexpr int RPB = block_of(TPR) / TPR;
     __shared__ float red[RPB][2][TPR / 32];
     const int tid = threadIdx.x % TPR, sub = threadIdx.x / TPR, nv = cols / 16;
+    pdl_wait();
+    pdl_launch();
     const int n = used != nullptr ? min(rows, *used) : rows;
     const int step = gridDim.x * RPB;
     int row = blockIdx.x * RPB + sub;
@@ -236,12 +238,12 @@ template <typename T>
 cudaError_t quantize_t(const T* x, int rows, int cols, const int32_t* used, int8_t* q, float* scale, cudaStream_t st) {
     const int tpr = threads_of<T>(cols);
     const dim3 grid(grid_of(rows, tpr)), block(block_of(tpr));
-    if (tpr == 32) return launch_k(quantize_kernel<T, 32>, grid, block, 0, st, x, rows, cols, used, q, scale);
-    if (tpr == 64) return launch_k(quantize_kernel<T, 64>, grid, block, 0, st, x, rows, cols, used, q, scale);
-    if (tpr == 128) return launch_k(quantize_kernel<T, 128>, grid, block, 0, st, x, rows, cols, used, q, scale);
+    if (tpr == 32) return launch_dep(quantize_kernel<T, 32>, grid, block, 0, st, x, rows, cols, used, q, scale);
+    if (tpr == 64) return launch_dep(quantize_kernel<T, 64>, grid, block, 0, st, x, rows, cols, used, q, scale);
+    if (tpr == 128) return launch_dep(quantize_kernel<T, 128>, grid, block, 0, st, x, rows, cols, used, q, scale);
     if constexpr (sizeof(T) == 4)
-        if (tpr == 512) return launch_k(quantize_kernel<T, 512>, grid, block, 0, st, x, rows, cols, used, q, scale);
-    return launch_k(quantize_kernel<T, 256>, grid, block, 0, st, x, rows, cols, used, q, scale);
+        if (tpr == 512) return launch_dep(quantize_kernel<T, 512>, grid, block, 0, st, x, rows, cols, used, q, scale);
+    return launch_dep(quantize_kernel<T, 256>, grid, block, 0, st, x, rows, cols, used, q, scale);
 }
 
 // ---- permutation with the rows in 8 bits ------------------------------------------
@@ -290,6 +292,7 @@ i8_count_kernel(const int32_t* __restrict__ idx, int T, int k, int kk, int E, in
                 int32_t* __restrict__ pos) {
     __shared__ int cnt[kMaxSlotCounts];
     __shared__ int s_idx[kChunk * MOE_MAX_K];
+    pdl_wait();
     pdl_launch();
     const int chunk = blockIdx.x, t0 = chunk * kChunk, n = min(kChunk, T - t0) * k;
     for (int i = threadIdx.x; i < E * kk; i += kCountThreads) cnt[i] = 0;
@@ -402,6 +405,8 @@ permute_i8_kernel(const __grid_constant__ PermuteArgs a) {
     const int step = gridDim.x * kTokens;
     int t = blockIdx.x * kTokens + sub;
     auto row_of = [&](int tok) { return static_cast<const T*>(a.x) + static_cast<size_t>(tok) * a.d; };
+    pdl_wait();   // !FEW: the chunk bases and indptr come from the scan
+    pdl_launch();
     Vec16<T> A[kHold<T>], B[kHold<T>];
     if (t < a.T) hold_row<T, TPR>(A, row_of(t), nv, tid);
     const int np = a.T * a.k;
@@ -456,8 +461,6 @@ permute_i8_kernel(const __grid_constant__ PermuteArgs a) {
                 }
             }
         }
-    } else {
-        pdl_wait();   // the chunk bases and indptr come from the scan
     }
     __syncthreads();
     if (a.pad > 0) {
@@ -549,12 +552,12 @@ template <typename T, bool FEW>
 cudaError_t permute_t(const PermuteArgs& a, cudaStream_t st) {
     const int tpr = threads_of<T>(a.d);
     const dim3 grid(grid_of(a.T, tpr)), block(block_of(tpr));
-    if (tpr == 32) return launch_k(permute_i8_kernel<T, 32, FEW>, grid, block, 0, st, a);
-    if (tpr == 64) return launch_k(permute_i8_kernel<T, 64, FEW>, grid, block, 0, st, a);
-    if (tpr == 128) return launch_k(permute_i8_kernel<T, 128, FEW>, grid, block, 0, st, a);
+    if (tpr == 32) return launch_dep(permute_i8_kernel<T, 32, FEW>, grid, block, 0, st, a);
+    if (tpr == 64) return launch_dep(permute_i8_kernel<T, 64, FEW>, grid, block, 0, st, a);
+    if (tpr == 128) return launch_dep(permute_i8_kernel<T, 128, FEW>, grid, block, 0, st, a);
     if constexpr (sizeof(T) == 4)
-        if (tpr == 512) return launch_k(permute_i8_kernel<T, 512, FEW>, grid, block, 0, st, a);
-    return launch_k(permute_i8_kernel<T, 256, FEW>, grid, block, 0, st, a);
+        if (tpr == 512) return launch_dep(permute_i8_kernel<T, 512, FEW>, grid, block, 0, st, a);
+    return launch_dep(permute_i8_kernel<T, 256, FEW>, grid, block, 0, st, a);
 }
 
 }  // namespace
@@ -573,14 +576,10 @@ cudaError_t launch_permute_i8(const PermuteI8& p, cudaStream_t st) {
     a.NB = ceil_div(p.T, kChunk);
     const bool few = static_cast<long long>(p.T) * p.k <= kFewPairs;
     if (few) return p.dtype == MOE_DTYPE_BF16 ? permute_t<__nv_bfloat16, true>(a, st) : permute_t<float, true>(a, st);
-    cudaError_t e = launch_k(i8_count_kernel, dim3(a.NB), dim3(kCountThreads), 0, st, p.idx, p.T, p.k, p.kk, p.E, a.NB,
+    cudaError_t e = launch_dep(i8_count_kernel, dim3(a.NB), dim3(kCountThreads), 0, st, p.idx, p.T, p.k, p.kk, p.E, a.NB,
                              p.blockcnt, p.pos);
     if (e != cudaSuccess) return e;
-    struct Dependent {   // each later launch starts beside the one before and waits for it
-        Dependent() { g_pdl = true; }
-        ~Dependent() { g_pdl = false; }
-    } dependent;
-    e = launch_k(i8_scan_kernel, dim3(1), dim3(kScan8Threads), 0, st, a, static_cast<const int32_t*>(p.blockcnt), p.blockoff);
+    e = launch_dep(i8_scan_kernel, dim3(1), dim3(kScan8Threads), 0, st, a, static_cast<const int32_t*>(p.blockcnt), p.blockoff);
     if (e != cudaSuccess) return e;
     return p.dtype == MOE_DTYPE_BF16 ? permute_t<__nv_bfloat16, false>(a, st) : permute_t<float, false>(a, st);
 }

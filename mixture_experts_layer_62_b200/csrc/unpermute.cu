@@ -102,6 +102,8 @@ constexpr int kMixThreads = 128;
 template <typename T, bool GATED, bool DROP, int K>
 __global__ void __launch_bounds__(kMixThreads)
 mix_kernel(const __grid_constant__ MixArgs a, int slices) {
+    pdl_wait();
+    pdl_launch();
     const size_t t = blockIdx.x / slices;
     const int sl = static_cast<int>(blockIdx.x - t * slices), nvec = a.d / 8;
     const int v_lo = static_cast<int>(static_cast<long long>(nvec) * sl / slices);
@@ -162,6 +164,8 @@ template <typename T, bool DROP, int K, int THREADS>
 __global__ void __launch_bounds__(THREADS)
 mix_back_kernel(const __grid_constant__ MixBackArgs a) {
     __shared__ float part[THREADS / 32][K];
+    pdl_wait();
+    pdl_launch();
     const int nvec = a.d / 8;
     T* dO = static_cast<T*>(a.dO);
     if (blockIdx.x >= a.T) {
@@ -231,7 +235,7 @@ mix_back_kernel(const __grid_constant__ MixBackArgs a) {
 template <typename T, bool DROP, int K>
 cudaError_t mix_back_k(const MixBackArgs& a, cudaStream_t st) {
     const unsigned grid = static_cast<unsigned>(a.T) + (a.row_token != nullptr ? kPadBlocks : 0);
-    return launch_k(mix_back_kernel<T, DROP, K, 128>, dim3(grid), dim3(128), 0, st, a);
+    return launch_dep(mix_back_kernel<T, DROP, K, 128>, dim3(grid), dim3(128), 0, st, a);
 }
 template <typename T, bool DROP>
 cudaError_t mix_back_t(const MixBackArgs& a, cudaStream_t st) {
@@ -248,11 +252,11 @@ cudaError_t mix_d(const MixArgs& a, cudaStream_t st) {
     int slices = 1;
     while (a.T * slices < 2 * 148 && slices * kMixThreads < a.d / 8) slices *= 2;
     const dim3 grid(static_cast<unsigned>(a.T) * slices), block(kMixThreads);
-    if (a.k <= 1) return launch_k(mix_kernel<T, GATED, DROP, 1>, grid, block, 0, st, a, slices);
-    if (a.k <= 2) return launch_k(mix_kernel<T, GATED, DROP, 2>, grid, block, 0, st, a, slices);
-    if (a.k <= 4) return launch_k(mix_kernel<T, GATED, DROP, 4>, grid, block, 0, st, a, slices);
-    if (a.k <= 8) return launch_k(mix_kernel<T, GATED, DROP, 8>, grid, block, 0, st, a, slices);
-    return launch_k(mix_kernel<T, GATED, DROP, 16>, grid, block, 0, st, a, slices);
+    if (a.k <= 1) return launch_dep(mix_kernel<T, GATED, DROP, 1>, grid, block, 0, st, a, slices);
+    if (a.k <= 2) return launch_dep(mix_kernel<T, GATED, DROP, 2>, grid, block, 0, st, a, slices);
+    if (a.k <= 4) return launch_dep(mix_kernel<T, GATED, DROP, 4>, grid, block, 0, st, a, slices);
+    if (a.k <= 8) return launch_dep(mix_kernel<T, GATED, DROP, 8>, grid, block, 0, st, a, slices);
+    return launch_dep(mix_kernel<T, GATED, DROP, 16>, grid, block, 0, st, a, slices);
 }
 template <typename T>
 cudaError_t mix_t(const MixArgs& a, cudaStream_t st) {
