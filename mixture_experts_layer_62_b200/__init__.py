@@ -376,16 +376,22 @@ def _device(t) -> int:
     return torch._C._cuda_getDevice()
 
 
-def _at(t, dev):
-    """Address of a tensor of the current device (None: NULL)."""
-    if t is None:
-        return None
+def _arg(t, dtype, numel, name, dev):
+    """Address of a tensor of the current device with at least numel elements
+    of dtype (another type, or fewer, would be read as something else or past
+    the end)."""
+    if t.dtype is not dtype or t.numel() < numel:
+        raise ValueError(f"{name}: expected {dtype} with at least {numel} elements, got {t.dtype} with {t.numel()}")
     if t.get_device() != dev:
-        raise ValueError(f"tensors passed to the MoE library must be CUDA tensors of the current device (cuda:{dev}), "
-                         f"got one on {t.device}")
+        raise ValueError(f"{name}: tensors passed to the MoE library must be CUDA tensors of the current device "
+                         f"(cuda:{dev}), got one on {t.device}")
     if not t.is_contiguous():
-        raise ValueError("tensors passed to the MoE library must be contiguous")
+        raise ValueError(f"{name}: tensors passed to the MoE library must be contiguous")
     return t.data_ptr()
+
+
+def _opt(t, dtype, numel, name, dev):
+    return None if t is None else _arg(t, dtype, numel, name, dev)
 
 
 def _on(stream, dev):
@@ -394,18 +400,12 @@ def _on(stream, dev):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _typed(t, dtype, numel, name):
-    """A tensor of another type or too small would be read as something else, or past its end."""
-    if t.dtype is not dtype or t.numel() < numel:
-        raise ValueError(f"{name}: expected {dtype} with at least {numel} elements, got {t.dtype} with {t.numel()}")
-
-
 def _rows(p: Problem) -> int:
     """permuted_rows without the call (p is checked by the library)."""
     return p.T * p.k + (p.E * (p.pad_rows - 1) if p.pad_rows > 0 else 0)
 
 
-_I8, _I32, _F32 = torch.int8, torch.int32, torch.float32
+_I8, _I32, _F32, _U8 = torch.int8, torch.int32, torch.float32, torch.uint8
 
 
 # ---- experts in 8-bit integers ------------------------------------------------
@@ -436,20 +436,16 @@ def quantize_rows(x, q=None, scale=None, used=None, stream=None):
     """Rows of x [..., cols] in 8 bits with a scale for each row (see
     moe_quantize_rows); used: a one-element int32 tensor, the rows to take.
     Returns (q, scale), allocated here when not given."""
-    cols = x.shape[-1]
-    rows = x.numel() // cols if cols else 0
+    dev = _device(x)
+    dt, n, cols = x.dtype, x.numel(), x.shape[-1]
+    rows = n // cols if cols else 0
     if q is None:
         q = torch.empty(x.shape, dtype=_I8, device=x.device)
     if scale is None:
         scale = torch.empty(x.shape[:-1], dtype=_F32, device=x.device)
-    _typed(q, _I8, rows * cols, "q")
-    _typed(scale, _F32, rows, "scale")
-    if used is not None:
-        _typed(used, _I32, 1, "used")
-    code = _dtype_code(x.dtype)
-    dev = _device(x)
-    rc = _lib().moe_quantize_rows(code, _at(x, dev), rows, cols, _at(used, dev), _at(q, dev), _at(scale, dev),
-                                  _on(stream, dev))
+    rc = _lib().moe_quantize_rows(_dtype_code(dt), _arg(x, dt, n, "x", dev), rows, cols,
+                                  _opt(used, _I32, 1, "used", dev), _arg(q, _I8, n, "q", dev),
+                                  _arg(scale, _F32, rows, "scale", dev), _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_quantize_rows")
     return q, scale
@@ -457,83 +453,63 @@ def quantize_rows(x, q=None, scale=None, used=None, stream=None):
 
 def permute_int8(p: Problem, x, idx, pos, indptr, row_token, xq, xs, stats, workspace, stream=None):
     """moe_permute with the token rows in 8 bits (see moe_permute_int8)."""
-    rows, pairs = _rows(p), p.T * p.k
-    _typed(x, torch_dtype(p.dtype), p.T * p.d, "x")
-    _typed(idx, _I32, pairs, "idx")
-    _typed(pos, _I32, pairs, "pos")
-    _typed(indptr, _I32, p.E + 1, "indptr")
-    _typed(row_token, _I32, rows, "row_token")
-    _typed(xq, _I8, rows * p.d, "xq")
-    _typed(xs, _F32, rows, "xs")
-    _typed(stats, torch.uint8, STATS_HEADER_BYTES + 16 * p.E, "stats")
-    dev = _device(x)
-    rc = _lib().moe_permute_int8(ctypes.byref(p), _at(x, dev), _at(idx, dev), _at(pos, dev), _at(indptr, dev),
-                                 _at(row_token, dev), _at(xq, dev), _at(xs, dev), _at(stats, dev), _at(workspace, dev),
-                                 workspace.nbytes, _on(stream, dev))
+    dev, T, d, E = _device(x), p.T, p.d, p.E
+    rows, pairs = _rows(p), T * p.k
+    rc = _lib().moe_permute_int8(
+        ctypes.byref(p), _arg(x, torch_dtype(p.dtype), T * d, "x", dev), _arg(idx, _I32, pairs, "idx", dev),
+        _arg(pos, _I32, pairs, "pos", dev), _arg(indptr, _I32, E + 1, "indptr", dev),
+        _arg(row_token, _I32, rows, "row_token", dev), _arg(xq, _I8, rows * d, "xq", dev),
+        _arg(xs, _F32, rows, "xs", dev), _arg(stats, _U8, STATS_HEADER_BYTES + 16 * E, "stats", dev),
+        _arg(workspace, _U8, 0, "workspace", dev), workspace.nbytes, _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_permute_int8")
 
 
 def expert_up_int8(p: Problem, xq, xs, indptr, W1, w1s, W3, w3s, h, workspace, stats=None, stream=None):
     """h = SiLU(a) b over 8-bit rows and weights with their scales; see moe_expert_up_int8."""
-    rows, E, d, dff = _rows(p), p.E, p.d, p.d_ff
-    _typed(xq, _I8, rows * d, "xq")
-    _typed(xs, _F32, rows, "xs")
-    _typed(indptr, _I32, E + 1, "indptr")
-    _typed(W1, _I8, E * dff * d, "W1")
-    _typed(w1s, _F32, E * dff, "w1s")
-    _typed(W3, _I8, E * dff * d, "W3")
-    _typed(w3s, _F32, E * dff, "w3s")
-    _typed(h, torch_dtype(p.dtype), rows * dff, "h")
-    dev = _device(xq)
-    rc = _lib().moe_expert_up_int8(ctypes.byref(p), _at(xq, dev), _at(xs, dev), _at(indptr, dev), _at(W1, dev),
-                                   _at(w1s, dev), _at(W3, dev), _at(w3s, dev), _at(h, dev), _at(stats, dev),
-                                   _at(workspace, dev), workspace.nbytes, _on(stream, dev))
+    dev, rows, E, d, dff = _device(xq), _rows(p), p.E, p.d, p.d_ff
+    n = E * dff
+    rc = _lib().moe_expert_up_int8(
+        ctypes.byref(p), _arg(xq, _I8, rows * d, "xq", dev), _arg(xs, _F32, rows, "xs", dev),
+        _arg(indptr, _I32, E + 1, "indptr", dev), _arg(W1, _I8, n * d, "W1", dev), _arg(w1s, _F32, n, "w1s", dev),
+        _arg(W3, _I8, n * d, "W3", dev), _arg(w3s, _F32, n, "w3s", dev),
+        _arg(h, torch_dtype(p.dtype), rows * dff, "h", dev),
+        _opt(stats, _U8, STATS_HEADER_BYTES, "stats", dev), _arg(workspace, _U8, 0, "workspace", dev),
+        workspace.nbytes, _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_expert_up_int8")
 
 
 def expert_down_int8(p: Problem, hq, hs, indptr, W2, w2s, o, workspace, stats=None, stream=None):
     """o = hq W2^T over 8-bit rows and weights with their scales; see moe_expert_down_int8."""
-    rows, E, d, dff = _rows(p), p.E, p.d, p.d_ff
-    _typed(hq, _I8, rows * dff, "hq")
-    _typed(hs, _F32, rows, "hs")
-    _typed(indptr, _I32, E + 1, "indptr")
-    _typed(W2, _I8, E * d * dff, "W2")
-    _typed(w2s, _F32, E * d, "w2s")
-    _typed(o, torch_dtype(p.dtype), rows * d, "o")
-    dev = _device(hq)
-    rc = _lib().moe_expert_down_int8(ctypes.byref(p), _at(hq, dev), _at(hs, dev), _at(indptr, dev), _at(W2, dev),
-                                     _at(w2s, dev), _at(o, dev), _at(stats, dev), _at(workspace, dev),
-                                     workspace.nbytes, _on(stream, dev))
+    dev, rows, E, d, dff = _device(hq), _rows(p), p.E, p.d, p.d_ff
+    n = E * d
+    rc = _lib().moe_expert_down_int8(
+        ctypes.byref(p), _arg(hq, _I8, rows * dff, "hq", dev), _arg(hs, _F32, rows, "hs", dev),
+        _arg(indptr, _I32, E + 1, "indptr", dev), _arg(W2, _I8, n * dff, "W2", dev), _arg(w2s, _F32, n, "w2s", dev),
+        _arg(o, torch_dtype(p.dtype), rows * d, "o", dev), _opt(stats, _U8, STATS_HEADER_BYTES, "stats", dev),
+        _arg(workspace, _U8, 0, "workspace", dev), workspace.nbytes, _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_expert_down_int8")
 
 
 # ---- the way back, with dropout, residual and gradients -------------------------
 
-def _rng(rng):
-    if rng is not None and (rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2):
-        raise ValueError("rng: expected two 64-bit integers (seed, offset)")
-    return rng
+def _rng(rng, dev):
+    """Address of the generator's {seed, offset}: two 64-bit integers."""
+    if rng is None:
+        return None
+    return _arg(rng, torch.uint64 if rng.dtype is torch.uint64 else torch.int64, 2, "rng", dev)
 
 
 def combine_dropout(p: Problem, o, pos, gate, out, s=None, residual=None, prob=0.0, rng=None, stream=None):
     """out_t = residual_t + dropout(sum_j gate[t,j] o[pos[t,j]] (+ s_t)); rng: a
     device tensor of two 64-bit integers (seed, offset). See moe_combine_dropout."""
-    dt, row, n = torch_dtype(p.dtype), _rows(p) * p.d, p.T * p.d
-    _typed(o, dt, row, "o")
-    _typed(pos, _I32, p.T * p.k, "pos")
-    _typed(gate, _F32, p.T * p.k, "gate")
-    _typed(out, dt, n, "out")
-    if s is not None:
-        _typed(s, dt, n, "s")
-    if residual is not None:
-        _typed(residual, dt, n, "residual")
-    _rng(rng)
-    dev = _device(o)
-    rc = _lib().moe_combine_dropout(ctypes.byref(p), _at(o, dev), _at(pos, dev), _at(gate, dev), _at(s, dev),
-                                    _at(residual, dev), prob, _at(rng, dev), _at(out, dev), _on(stream, dev))
+    dev, dt, n, pairs = _device(o), torch_dtype(p.dtype), p.T * p.d, p.T * p.k
+    rc = _lib().moe_combine_dropout(
+        ctypes.byref(p), _arg(o, dt, _rows(p) * p.d, "o", dev), _arg(pos, _I32, pairs, "pos", dev),
+        _arg(gate, _F32, pairs, "gate", dev), _opt(s, dt, n, "s", dev), _opt(residual, dt, n, "residual", dev), prob,
+        _rng(rng, dev), _arg(out, dt, n, "out", dev), _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_combine_dropout")
     return out
@@ -544,35 +520,25 @@ def combine_backward(p: Problem, dy, o, pos, gate, dO, dgate, ds=None, prob=0.0,
     """Gradients of combine_dropout with the same prob and rng values:
     dO[pos] = gate u, dgate = <u, o[pos]>, ds = u with u = dropout(dy); indptr
     and row_token are needed with p.pad_rows > 0. See moe_combine_backward."""
-    dt, row, n = torch_dtype(p.dtype), _rows(p) * p.d, p.T * p.d
-    _typed(dy, dt, n, "dy")
-    _typed(o, dt, row, "o")
-    _typed(pos, _I32, p.T * p.k, "pos")
-    _typed(gate, _F32, p.T * p.k, "gate")
-    _typed(dO, dt, row, "dO")
-    _typed(dgate, _F32, p.T * p.k, "dgate")
-    if ds is not None:
-        _typed(ds, dt, n, "ds")
-    if p.pad_rows > 0 and indptr is not None and row_token is not None:
-        _typed(indptr, _I32, p.E + 1, "indptr")
-        _typed(row_token, _I32, _rows(p), "row_token")
-    _rng(rng)
-    dev = _device(dy)
-    rc = _lib().moe_combine_backward(ctypes.byref(p), _at(dy, dev), _at(o, dev), _at(pos, dev), _at(gate, dev), prob,
-                                     _at(rng, dev), _at(indptr, dev), _at(row_token, dev), _at(dO, dev),
-                                     _at(dgate, dev), _at(ds, dev), _on(stream, dev))
+    dev, dt, n, pairs, rows = _device(dy), torch_dtype(p.dtype), p.T * p.d, p.T * p.k, _rows(p)
+    ends = tokens = None
+    if p.pad_rows > 0:
+        ends, tokens = _opt(indptr, _I32, p.E + 1, "indptr", dev), _opt(row_token, _I32, rows, "row_token", dev)
+    rc = _lib().moe_combine_backward(
+        ctypes.byref(p), _arg(dy, dt, n, "dy", dev), _arg(o, dt, rows * p.d, "o", dev),
+        _arg(pos, _I32, pairs, "pos", dev), _arg(gate, _F32, pairs, "gate", dev), prob, _rng(rng, dev), ends, tokens,
+        _arg(dO, dt, rows * p.d, "dO", dev), _arg(dgate, _F32, pairs, "dgate", dev), _opt(ds, dt, n, "ds", dev),
+        _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_combine_backward")
 
 
 def permute_backward(p: Problem, dxp, pos, dx, stream=None):
     """dx_t = sum_j dxp[pos[t,j]] over the kept pairs; see moe_permute_backward."""
-    dt = torch_dtype(p.dtype)
-    _typed(dxp, dt, _rows(p) * p.d, "dxp")
-    _typed(pos, _I32, p.T * p.k, "pos")
-    _typed(dx, dt, p.T * p.d, "dx")
-    dev = _device(dxp)
-    rc = _lib().moe_permute_backward(ctypes.byref(p), _at(dxp, dev), _at(pos, dev), _at(dx, dev), _on(stream, dev))
+    dev, dt = _device(dxp), torch_dtype(p.dtype)
+    rc = _lib().moe_permute_backward(ctypes.byref(p), _arg(dxp, dt, _rows(p) * p.d, "dxp", dev),
+                                     _arg(pos, _I32, p.T * p.k, "pos", dev), _arg(dx, dt, p.T * p.d, "dx", dev),
+                                     _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_permute_backward")
     return dx

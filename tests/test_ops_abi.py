@@ -105,16 +105,44 @@ def test_gradient_refusals():
         assert call("moe_permute_backward", p, *with_(args, i, ODD)) == moe.MOE_ERR_INVALID_ARG
 
 
-def test_binding_refuses_what_it_can_see():
+class FakeCuda:
+    """What the binding asks of a tensor, without a GPU."""
+
+    def __init__(self, dtype, n, dev=0, contiguous=True):
+        self.dtype, self.n, self.dev, self.c = dtype, n, dev, contiguous
+        self.device, self.is_cuda, self.nbytes = f"cuda:{dev}", True, n
+
+    def numel(self):
+        return self.n
+
+    def get_device(self):
+        return self.dev
+
+    def is_contiguous(self):
+        return self.c
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+def test_binding_refuses_what_it_can_see(monkeypatch):
     p = moe.problem(4, 64, 64, 2, 1)
     cpu = torch.zeros((4, 64), dtype=torch.bfloat16)
-    with pytest.raises(ValueError):
-        moe.quantize_rows(cpu)                                                    # not on the GPU
-    with pytest.raises(ValueError):
-        moe.quantize_rows(cpu, torch.zeros((4, 64)), torch.zeros(4))              # q is not int8
-    with pytest.raises(ValueError):
-        moe.quantize_rows(cpu, torch.zeros((3, 64), dtype=torch.int8), torch.zeros(4))
-    with pytest.raises(ValueError):
-        moe.expert_down_int8(p, torch.zeros((4, 64)), torch.zeros(4), None, None, None, cpu, cpu)
-    with pytest.raises(ValueError):
-        moe.combine_dropout(p, cpu, cpu, cpu, cpu, prob=0.5, rng=torch.zeros(2))
+    for call in (lambda: moe.quantize_rows(cpu), lambda: moe.combine_dropout(p, cpu, cpu, cpu, cpu),
+                 lambda: moe.permute_backward(p, cpu, cpu, cpu),
+                 lambda: moe.expert_down_int8(p, cpu, cpu, cpu, cpu, cpu, cpu, cpu)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    bf, i32, f32, i8, u8 = torch.bfloat16, torch.int32, torch.float32, torch.int8, torch.uint8
+    good = [FakeCuda(i8, 256), FakeCuda(f32, 4), FakeCuda(i32, 3), FakeCuda(i8, 8192), FakeCuda(f32, 128),
+            FakeCuda(bf, 256), FakeCuda(u8, 1 << 30)]
+    for i in range(7):
+        for bad in (FakeCuda(torch.float64, 1 << 30), FakeCuda(good[i].dtype, good[i].n, dev=1),
+                    FakeCuda(good[i].dtype, good[i].n, contiguous=False)) + \
+                (() if i == 6 else (FakeCuda(good[i].dtype, good[i].n - 1),)):
+            with pytest.raises(ValueError):
+                moe.expert_down_int8(p, *with_(good, i, bad))
+    with pytest.raises(ValueError, match="rng"):
+        moe.combine_dropout(p, FakeCuda(bf, 256), FakeCuda(i32, 4), FakeCuda(f32, 4), FakeCuda(bf, 256), prob=0.5,
+                            rng=FakeCuda(f32, 2))
