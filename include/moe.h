@@ -334,8 +334,8 @@ int moe_bias_update(const moe_problem* p, const void* stats, float gamma, float*
  * decided exactly, so q depends on x alone. A row with a_r < 2^-100 gives
  * zeros and scale 0. x [rows, cols] of dtype MOE_DTYPE_*, q [rows, cols],
  * scale [rows]; cols % 16 == 0 (else MOE_ERR_UNSUPPORTED).
- * used: NULL, or one device integer: only the first min(rows, *used) rows are
- * read and written, the others stay as they are (pass &indptr[E] for the
+ * used: NULL, or one device integer: only the first min(rows, *used) rows
+ * count, the others of q and scale stay as they are (pass &indptr[E] for the
  * hidden rows of a layer). */
 int moe_quantize_rows(int32_t dtype, const void* x, int32_t rows, int32_t cols, const int32_t* used,
                       int8_t* q, float* scale, void* stream);

@@ -918,8 +918,8 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 // First launch of a product: the status word is MOE_OK, and the arrival
 // counters and sums of the tail tiles are zero, before the product passes its
 // wait. The product's launch and prologue run beside it and the kernel
-// before; neither product triggers a next launch early, so that a following
-// call's zeros cannot meet this one's sums.
+// before. It waits itself before it writes: a product still running on the
+// same workspace has completed by then.
 __global__ void __launch_bounds__(256) i8_begin_kernel(const KP p, int grid) {
     __shared__ Ctl<1> c;
     pdl_launch();

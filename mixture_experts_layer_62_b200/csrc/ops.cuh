@@ -11,8 +11,9 @@ namespace moe {
 // the kernel's own launch and prologue overlap the end of the one before,
 // and it calls pdl_wait() (which returns when everything before has completed
 // and is visible) in every thread before it touches global memory, so calls
-// order as ever. Kernels launched this way call pdl_launch() early for the
-// next one, except where two calls could share a workspace.
+// order as ever. The short kernels call pdl_launch() early for the next one;
+// the products do not (a next product's first kernel waiting beside them cost
+// 1 us of 43 where it should have saved some).
 struct DependentLaunch {
     DependentLaunch() : was(g_pdl) { g_pdl = true; }
     ~DependentLaunch() { g_pdl = was; }

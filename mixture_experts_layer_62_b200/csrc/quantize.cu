@@ -214,12 +214,13 @@ quantize_kernel(const T* __restrict__ x, int rows, int cols, const int32_t* __re
     const int tid = threadIdx.x % TPR, sub = threadIdx.x / TPR, nv = cols / 16;
     pdl_wait();
     pdl_launch();
-    const int n = used != nullptr ? min(rows, *used) : rows;
     const int step = gridDim.x * RPB;
     int row = blockIdx.x * RPB + sub;
     auto at = [&](int r) { return x + static_cast<size_t>(r) * cols; };
     Vec16<T> A[kHold<T>], B[kHold<T>];
-    if (row < n) hold_row<T, TPR>(A, at(row), nv, tid);
+    // the first row's reads start beside that of *used (a row that is not used is read for nothing)
+    if (row < rows) hold_row<T, TPR>(A, at(row), nv, tid);
+    const int n = used != nullptr ? min(rows, *used) : rows;
     // the threads of a row leave together
     auto one = [&](const Vec16<T> (&cur)[kHold<T>], Vec16<T> (&next)[kHold<T>], int half) {
         if (step < n - row) hold_row<T, TPR>(next, at(row + step), nv, tid);

@@ -428,3 +428,64 @@ def test_bad_offsets_are_left_out():
         r = (q[lo:hi].double() @ W[e].double().T) * s[lo:hi, None].double()
         assert ((o[lo:hi].double() - r).abs() <= R.plain_bound(r, torch.bfloat16)).all()
     assert (o[20:30] == 7.0).all()
+
+
+def test_calls_wait_for_what_comes_before_them():
+    # the kernels start early beside the work before them; what they read has
+    # to be there all the same: behind a slow producer on their own stream, on
+    # another one (an event between them), and in a graph with a fork and a join
+    g = gen(3)
+    rows, cols, N = 300, 2048, 512
+    src = randn(g, rows, cols).to(torch.bfloat16)
+    x, q, s = torch.zeros_like(src), torch.zeros((rows, cols), dtype=torch.int8, device=DEV), torch.zeros(rows, device=DEV)
+    W, ws_ = ints(g, 1, N, cols), torch.ones((1, N), device=DEV)
+    p = moe.problem(rows, N, cols, 1, 1)
+    work, o = moe.alloc_int8_workspace(p, DEV), torch.zeros((rows, N), dtype=torch.bfloat16, device=DEV)
+    indptr = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    moe.quantize_rows(src, q, s)
+    moe.expert_down_int8(p, q, s, indptr, W, ws_, o, work)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (q, s, o)]
+
+    def consume():
+        moe.quantize_rows(x, q, s)
+        moe.expert_down_int8(p, q, s, indptr, W, ws_, o, work)
+
+    def produce():
+        torch.cuda._sleep(2_000_000)    # about a millisecond
+        x.copy_(src)
+
+    def check():
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((q, s, o), want))
+        for t in (x, q, s, o):
+            t.zero_()
+        torch.cuda.synchronize()
+
+    other = torch.cuda.Stream()
+    check()
+    for _ in range(3):
+        produce()
+        consume()
+        check()
+        moe.quantize_rows(src, q, s)    # a kernel of the library's own before the wait for the event
+        with torch.cuda.stream(other):
+            produce()
+            done = other.record_event()
+        torch.cuda.current_stream().wait_event(done)
+        consume()
+        check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        fork = main.record_event()
+        other.wait_event(fork)
+        with torch.cuda.stream(other):
+            produce()
+            done = other.record_event()
+        moe.quantize_rows(src, q, s)
+        main.wait_event(done)
+        consume()
+    for _ in range(3):
+        graph.replay()
+        check()
