@@ -91,26 +91,36 @@ __device__ __forceinline__ void list_tiles(Ctl<STAGES>* c, const KP& p, int tile
     const int lane = threadIdx.x & 31;
     int base = 0;
     bool bad = false;
-    for (int g0 = 0; g0 < p.E; g0 += 32) {
-        const int g = g0 + lane;
-        int v = 0;
-        if (g < p.E) {
-            const int lo = p.indptr[g], hi = p.indptr[g + 1];
-            const bool ok = lo >= 0 && hi >= lo && hi <= p.rows;
-            const int n = ok ? hi - lo : 0;
-            bad |= !ok;
-            c->row0[g] = lo;
-            c->nrow[g] = n;
-            v = (n + tile_m - 1) / tile_m * p.nt;
-        }
-        int incl = v;
+    // eight times 32 groups' offsets requested at once: one memory round trip up to 256 experts
+    for (int b0 = 0; b0 < p.E; b0 += 256) {
+        int lo[8], hi[8];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
+        for (int i = 0; i < 8; ++i) {
+            const int g = b0 + 32 * i + lane;
+            lo[i] = g < p.E ? p.indptr[g] : 0;
+            hi[i] = g < p.E ? p.indptr[g + 1] : 0;
         }
-        if (g < p.E) c->cum[g] = base + incl - v;
-        base += __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int g = b0 + 32 * i + lane;
+            if (b0 + 32 * i >= p.E) break;
+            const bool ok = lo[i] >= 0 && hi[i] >= lo[i] && hi[i] <= p.rows;
+            const int n = ok ? hi[i] - lo[i] : 0;
+            bad |= !ok;
+            const int v = (n + tile_m - 1) / tile_m * p.nt;
+            int incl = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += u;
+            }
+            if (g < p.E) {
+                c->row0[g] = lo[i];
+                c->nrow[g] = n;
+                c->cum[g] = base + incl - v;
+            }
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
     }
     if (lane == 0) c->cum[p.E] = base;
     if (kDebugChecks && __any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) debug_record_bounds(p.status);
