@@ -7,18 +7,26 @@
 // of the kernel changes a bit of the result; the float factors are applied
 // as (float(sum) * sa) * sb and the result is rounded once.
 //
-// Both forms here are persistent kernels of six warps: one loads by TMA into
-// a ring of 128-byte K blocks (128-byte swizzle), one issues the MMAs, four
-// read the accumulators back (tcgen05.ld), apply the scales and store, while
-// the next tile runs into the other accumulator. The tile list is formed in
-// each CTA's shared memory from the group offsets. Every wait is bounded
-// (moe_set_wait_limit): on expiry the CTA records MOE_ERR_TIMEOUT, lets what
-// it started land, frees its tensor memory and returns.
-//  * pair: clusters of two CTAs share tiles of 256 rows of A x 256 weight
-//    rows (cta_group::2), each CTA loading half of both, which halves the
-//    bytes a CTA brings in for the same products; groups of many rows.
+// Two forms, both persistent kernels: one warp loads by TMA into a ring of
+// 128-byte K blocks (128-byte swizzle), one issues the MMAs, four (single) or
+// eight (pair) read the accumulators back (tcgen05.ld), apply the scales and
+// store, while the next tile runs into the other accumulator. The tile list
+// is formed in each CTA's shared memory from the group offsets. Every wait is
+// bounded (moe_set_wait_limit): on expiry the CTA records MOE_ERR_TIMEOUT,
+// lets what it started land, frees its tensor memory and returns.
+//  * pair: clusters of two CTAs share tiles of 256 rows of A x 512 weight
+//    rows (cta_group::2), each CTA loading half of both; groups of many rows.
+//    Bound by the tensor pipe and the board's power: 8192 rows, K = 14336,
+//    18944 channels run at 3.3 P operations/s, twice the measured bf16 GEMM
+//    rate; with K = 4096 (Mixtral-shaped up projection, 8 experts, 700 us, 2.75
+//    P/s) the SwiGLU epilogue and the ragged blocks show. What the tile's
+//    width buys: with 256 x 256 tiles the L2 has to deliver a third more bytes
+//    for the same products, and K = 14336 took 1449 us instead of 1365.
 //  * single: one CTA a tile of 256 weight rows and up to 128 rows of A, for
-//    groups of few rows: the weights bound it.
+//    groups of few rows. Bound by the weight stream: 24 tokens of the
+//    Mixtral-shaped up projection (941 MB) take 141 us, 6.7 TB/s; 256 experts
+//    of 64 rows (7.5 GB) 1.19 ms, 98 % of the measured copy bandwidth, with DRAM
+//    traffic equal to the bytes of the operands.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -278,9 +286,9 @@ __device__ __forceinline__ void stage16(uint8_t* st, int row, int p0, const floa
 // q = 0, 1) hold the gates and lanes 64..127 (q = 2, 3) the up values of the
 // same channels; warps q and q + 2 trade halves of every 32 columns through
 // shared memory: each sends 16, receives 16, and finishes 16 rows of its 32
-// channels. (That trade is why whole tiles are not laid out this way too:
-// its shared-memory traffic slows the products beside it, 731 us against
-// PAIRUP for the Mixtral-shaped up projection of 8192 rows.)
+// channels. (That trade is why whole tiles are not laid out this way too: it
+// made the up projection of 8192 rows take 731 us instead of 710.) kShort
+// between 64 and 192 measures the same within 2 %, 255 costs 3 to 5 %.
 // Eight warps share the epilogue, two to a quarter of the lanes.
 // The tiles that do not fill a whole wave run as two items of 128 rows each
 // when that still fits in one wave.
