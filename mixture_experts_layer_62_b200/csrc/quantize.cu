@@ -46,12 +46,14 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
-// 16 consecutive elements of a row
+// 16 consecutive elements of a row, read past L1: each is read once, and a
+// kernel that started beside the one that writes its rows must not ask for
+// them as constants (so no __restrict__ on what it reads, either)
 template <typename T> struct Vec16;
 template <> struct Vec16<__nv_bfloat16> {
     uint32_t w[8];
     __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+        const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p)), b = __ldcg(reinterpret_cast<const uint4*>(p) + 1);
         w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
         w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
     }
@@ -70,7 +72,7 @@ template <> struct Vec16<float> {
     __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(p) + i);
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(p) + i);
             f[4 * i] = a.x; f[4 * i + 1] = a.y; f[4 * i + 2] = a.z; f[4 * i + 3] = a.w;
         }
     }
@@ -143,7 +145,8 @@ __device__ __forceinline__ uint4 quant16(const V& x, float a, float inv) {
 // shared memory when TPR > 32, another half of it for every other row; the
 // row's threads meet at a barrier of their own. Returns scale_r; put(v, w)
 // stores vector v.
-// the TPR threads of one row (of the block's block_of(TPR) / TPR)
+
+// The TPR threads of one row meet (a block has block_of(TPR) / TPR rows).
 template <int TPR>
 __device__ __forceinline__ void row_barrier() {
     if constexpr (TPR == 32) __syncwarp();
@@ -151,13 +154,13 @@ __device__ __forceinline__ void row_barrier() {
 }
 template <typename T> constexpr int kHold = sizeof(T) == 2 ? 4 : 2;   // registers: 32 a buffer
 template <typename T, int TPR>
-__device__ __forceinline__ void hold_row(Vec16<T> (&held)[kHold<T>], const T* __restrict__ xr, int nv, int tid) {
+__device__ __forceinline__ void hold_row(Vec16<T> (&held)[kHold<T>], const T* xr, int nv, int tid) {
 #pragma unroll
     for (int h = 0; h < kHold<T>; ++h)
         if (tid + h * TPR < nv) held[h].load(xr + static_cast<size_t>(tid + h * TPR) * 16);
 }
 template <typename T, int TPR, typename Put>
-__device__ __forceinline__ float quantize_row(const Vec16<T> (&held)[kHold<T>], const T* __restrict__ xr, int nv, int tid,
+__device__ __forceinline__ float quantize_row(const Vec16<T> (&held)[kHold<T>], const T* xr, int nv, int tid,
                                               float* red, Put put) {
     float a = 0.f;
 #pragma unroll
@@ -207,8 +210,7 @@ inline int grid_of(int rows, int tpr) {
 
 template <typename T, int TPR>
 __global__ void __launch_bounds__(block_of(TPR))
-quantize_kernel(const T* __restrict__ x, int rows, int cols, const int32_t* __restrict__ used, int8_t* __restrict__ q,
-                float* __restrict__ scale) {
+quantize_kernel(const T* x, int rows, int cols, const int32_t* used, int8_t* q, float* scale) {
     constexpr int RPB = block_of(TPR) / TPR;
     __shared__ float red[RPB][2][TPR / 32];
     const int tid = threadIdx.x % TPR, sub = threadIdx.x / TPR, nv = cols / 16;
@@ -289,8 +291,7 @@ __device__ __forceinline__ void write_header(const PermuteArgs& a, int kept, int
 // for the same rows: the same expert and, under the slot order, the same slot.
 constexpr int kCountThreads = 256;
 __global__ void __launch_bounds__(kCountThreads)
-i8_count_kernel(const int32_t* __restrict__ idx, int T, int k, int kk, int E, int NB, int32_t* __restrict__ blockcnt,
-                int32_t* __restrict__ pos) {
+i8_count_kernel(const int32_t* idx, int T, int k, int kk, int E, int NB, int32_t* blockcnt, int32_t* pos) {
     __shared__ int cnt[kMaxSlotCounts];
     __shared__ int s_idx[kChunk * MOE_MAX_K];
     pdl_wait();
@@ -319,8 +320,8 @@ i8_count_kernel(const int32_t* __restrict__ idx, int T, int k, int kk, int E, in
 // counts), then capacity, padded row offsets and statistics per expert.
 // A warp takes four experts at a time, so that their loads overlap.
 constexpr int kScan8Threads = 1024;
-__global__ void __launch_bounds__(kScan8Threads) i8_scan_kernel(const __grid_constant__ PermuteArgs a, const int32_t* __restrict__ blockcnt,
-                                                         int32_t* __restrict__ blockoff) {
+__global__ void __launch_bounds__(kScan8Threads) i8_scan_kernel(const __grid_constant__ PermuteArgs a, const int32_t* blockcnt,
+                                                                int32_t* blockoff) {
     __shared__ int s_cnt[MOE_MAX_E], s_held[32], s_red[3][32];
     pdl_wait();
     pdl_launch();
