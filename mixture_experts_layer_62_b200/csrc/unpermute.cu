@@ -158,8 +158,9 @@ mix_kernel(const __grid_constant__ MixArgs a, int slices) {
 // One block per token: a thread takes every THREADS-th vector of dy, forms
 // u = D(dy) once and serves all of the token's slots from it; the slots' dot
 // products are summed lane by lane, then over the block in a fixed order.
-// Blocks past the tokens fill the padding rows of dO with zeros.
-constexpr int kPadBlocks = 64;
+// With padding, the first kPadBlocks blocks fill the padding rows of dO with
+// zeros: a warp reads the tokens of 32 rows at once and writes those of none.
+constexpr int kPadBlocks = 148;
 template <typename T, bool DROP, int K, int THREADS>
 __global__ void __launch_bounds__(THREADS)
 mix_back_kernel(const __grid_constant__ MixBackArgs a) {
@@ -168,16 +169,20 @@ mix_back_kernel(const __grid_constant__ MixBackArgs a) {
     pdl_launch();
     const int nvec = a.d / 8;
     T* dO = static_cast<T*>(a.dO);
-    if (blockIdx.x >= a.T) {
-        const int used = min(a.indptr[a.E], a.rows);
-        float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int r = blockIdx.x - a.T; r < used; r += kPadBlocks)
-            if (a.row_token[r] < 0)
-                for (int v = threadIdx.x; v < nvec; v += THREADS)
-                    Vec8<T>::store(dO + static_cast<size_t>(r) * a.d + static_cast<size_t>(v) * 8, z);
+    const unsigned pads = a.row_token != nullptr ? kPadBlocks : 0u;
+    if (blockIdx.x < pads) {
+        const int used = min(a.indptr[a.E], a.rows), lane = threadIdx.x & 31;
+        const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const int warps = kPadBlocks * (THREADS / 32);
+        for (long long r0 = 32ll * (blockIdx.x + kPadBlocks * (threadIdx.x >> 5)); r0 < used; r0 += 32ll * warps) {
+            const bool none = r0 + lane < used && a.row_token[r0 + lane] < 0;
+            for (unsigned m = __ballot_sync(0xffffffffu, none); m != 0; m &= m - 1)
+                for (int v = lane; v < nvec; v += 32)
+                    Vec8<T>::store(dO + static_cast<size_t>(r0 + __ffs(m) - 1) * a.d + static_cast<size_t>(v) * 8, z);
+        }
         return;
     }
-    const size_t t = blockIdx.x;
+    const size_t t = blockIdx.x - pads;
     int p[K];
     float g[K], acc[K];
 #pragma unroll
