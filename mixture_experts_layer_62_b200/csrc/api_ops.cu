@@ -23,7 +23,7 @@ I8Layout make_i8_layout(const moe_problem& p) {
     const long long rows = permuted_rows(p);
     L.part_rows = (int)(rows < 128 ? (rows + 15) / 16 * 16 : 128);
     L.part = take((size_t)kI8MaxGrid * 256 * L.part_rows * 4);
-    L.sem = take((size_t)kI8MaxGrid * 4 * 4);
+    L.sem = take((size_t)kI8MaxGrid * 8 * 4);
     L.status = take(4);
     L.total = off;
     return L;

@@ -8,9 +8,8 @@
 // as (float(sum) * sa) * sb and the result is rounded once.
 //
 // Two forms, both persistent kernels: one warp loads by TMA into a ring of
-// 128-byte K blocks (128-byte swizzle), one issues the MMAs, four (single) or
-// eight (pair) read the accumulators back (tcgen05.ld), apply the scales and
-// store, while the next tile runs into the other accumulator. The tile list
+// 128-byte K blocks (128-byte swizzle), one issues the MMAs, eight read the
+// accumulators back (tcgen05.ld), apply the scales and store, while the next tile runs into the other accumulator. The tile list
 // is formed in each CTA's shared memory from the group offsets. Every wait is
 // bounded (moe_set_wait_limit): on expiry the CTA records MOE_ERR_TIMEOUT,
 // lets what it started land, frees its tensor memory and returns.
@@ -46,12 +45,12 @@ constexpr int BM = 128;                     // rows of A a CTA
 constexpr int A_BYTES = BM * BKB;           // 16 KB
 constexpr int BH_BYTES = 128 * BKB;         // 128 weight rows, 16 KB
 constexpr int ACC_COLS = 256, TMEM_COLS = 512;
-constexpr int NUM_THREADS = 192;
 constexpr int P_STAGES = 4, P_STAGE_BYTES = A_BYTES + 2 * BH_BYTES;
-constexpr int P_THREADS = 320;                      // pair: eight epilogue warps
+constexpr int NUM_THREADS = 320;                    // eight epilogue warps
 constexpr int P_XCH_FLOATS = 4 * 2 * 16 * 32;       // pair SWIGLU: [warp pair][direction][16 rows][32 channels]
 constexpr int P_SCALE_FLOATS = 8 * 128;             // pair: the channel scales of each epilogue warp's columns
 constexpr int S_STAGES = 4, S_STAGE_BYTES = A_BYTES + 2 * BH_BYTES;
+constexpr int S_ROW_FLOATS = 8 * 64;                // single: the row scales of each epilogue warp's columns
 constexpr long long kBandBytes = 32ll << 20;   // rows of A that a band of M blocks keeps in L2
 
 // kind::i8: A and B signed 8-bit, D signed 32-bit, both operands K-major
@@ -79,7 +78,7 @@ struct KP {
     int32_t* status;
     long long timeout_ns, drain_ns;
     int E, N, K, rows, nt, band_m;
-    int *part, *sem;   // single form: parts of the tail tiles [slots][part_rows][256] and arrivals [tail][4]
+    int *part, *sem;   // single form: parts of the tail tiles [slots][part_rows][256] and arrivals [tail][8]
     int part_rows;
 };
 
@@ -226,9 +225,18 @@ __device__ __forceinline__ float rcp(float x) {
 constexpr float kNegLog2e = -1.4426950408889634f;
 // SiLU(a) b = (a / (1 + exp(-a))) b. bf16 results: the fast exponential and
 // reciprocal (a few 2^-23 off, where the type rounds to 2^-8); fp32 results:
-// the accurate ones. exp(-a) overflowing gives a 0, as it should. The scalar
-// and the two-value form take the same roundings.
-__device__ __forceinline__ float swiglu(float a, float b, float*) { return a / (1.f + expf(-a)) * b; }
+// the accurate exponential, and the reciprocal of one unit in the last place
+// with subnormal results kept (a divide in its place took most of the
+// epilogue). exp(-a) overflowing gives a 0, as it should. The scalar and the
+// two-value form take the same roundings.
+__device__ __forceinline__ float rcp_full(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float swiglu(float a, float b, float*) {
+    return __fmul_rn(__fmul_rn(a, rcp_full(__fadd_rn(1.f, expf(-a)))), b);
+}
 __device__ __forceinline__ float swiglu(float a, float b, __nv_bfloat16*) {
     return __fmul_rn(__fmul_rn(a, rcp(__fadd_rn(1.f, ex2(__fmul_rn(a, kNegLog2e))))), b);
 }
@@ -440,9 +448,10 @@ __device__ __forceinline__ void short_swiglu(const KP& p, const Item& it, uint32
 }
 
 template <bool SWIGLU, typename OutT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-               const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmA32, const KP p) {
+               const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmA32,
+               const __grid_constant__ CUtensorMap, const KP p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* xch = reinterpret_cast<float*>(smem + P_STAGES * P_STAGE_BYTES);
@@ -737,6 +746,18 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, uint32_t (
         : "r"(t0), "r"(t1)
         : "memory");
 }
+// v[0..n) one under another
+template <typename OutT>
+__device__ __forceinline__ void put16(OutT* o, int stride, int n, const float* v) {
+    if (n == 16) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) put(o + static_cast<size_t>(j) * stride, v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 15; ++j)
+            if (j < n) put(o + static_cast<size_t>(j) * stride, v[j]);
+    }
+}
 __device__ __forceinline__ void red_add(int* p, uint32_t v) {
     asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
@@ -744,11 +765,13 @@ __device__ __forceinline__ void red_add(int* p, uint32_t v) {
 template <bool SWIGLU, typename OutT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-                 const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap, const KP p) {
+                 const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmB0h,
+                 const __grid_constant__ CUtensorMap tmB1h, const KP p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     using C = Ctl<S_STAGES>;
-    C* ctl = reinterpret_cast<C*>(smem + S_STAGES * S_STAGE_BYTES);
+    float* rows_sa = reinterpret_cast<float*>(smem + S_STAGES * S_STAGE_BYTES);
+    C* ctl = reinterpret_cast<C*>(rows_sa + S_ROW_FLOATS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = static_cast<int>(blockIdx.x);
 
@@ -759,7 +782,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&ctl->tfull[a], 1);
-            mbar_init(&ctl->tempty[a], 4);
+            mbar_init(&ctl->tempty[a], 8);
         }
         mbar_init(&ctl->drain, 1);
         ctl->abort_flag = 0;
@@ -789,17 +812,23 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 const Tile t = tile_of(ctl, p, w.tile, BM);
                 const int arow = t.row0 + t.m_blk * BM;
                 const int boxes = (min(t.rows - t.m_blk * BM, BM) + 31) / 32;
-                const int brow = t.g * p.N + (SWIGLU ? t.n_blk * 128 : t.n_blk * 256);
-                const int brow1 = SWIGLU ? brow : brow + 128;
-                const CUtensorMap* mb1 = SWIGLU ? &tmB1 : &tmB0;
+                // each half's weight rows in one box of 128, or of 64 where the expert has no more left: a 128-row
+                // box costs what it holds, two of 64 in its place 4 % (256 experts of 64 rows, 1158 -> 1203 us)
+                const int n0 = SWIGLU ? t.n_blk * 128 : t.n_blk * 256, n1 = SWIGLU ? n0 : n0 + 128;
+                const int brow = t.g * p.N + n0, brow1 = t.g * p.N + n1;
+                const CUtensorMap* m0 = p.N - n0 > 64 ? &tmB0 : &tmB0h;
+                const CUtensorMap* m1 = p.N - n1 > 64 ? (SWIGLU ? &tmB1 : &tmB0) : (SWIGLU ? &tmB1h : &tmB0h);
+                const bool two = n1 < p.N;
+                const uint32_t bytes = boxes * 32 * BKB + (p.N - n0 > 64 ? BH_BYTES : BH_BYTES / 2) +
+                                       (p.N - n1 > 64 ? BH_BYTES : two ? BH_BYTES / 2 : 0);
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     if (!wait_i8(&ctl->empty[s], ph ^ 1u, ctl, p)) { aborted = true; break; }
                     const uint32_t sa = smem_u32(smem + s * S_STAGE_BYTES);
-                    mbar_arrive_expect_tx(&ctl->full[s], 2 * BH_BYTES + boxes * 32 * BKB);
+                    mbar_arrive_expect_tx(&ctl->full[s], bytes);
                     armed |= 1u << s;
                     armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
-                    tma_load_2d(sa + A_BYTES, &tmB0, &ctl->full[s], kb * BKB, brow);
-                    tma_load_2d(sa + A_BYTES + BH_BYTES, mb1, &ctl->full[s], kb * BKB, brow1);
+                    tma_load_2d(sa + A_BYTES, m0, &ctl->full[s], kb * BKB, brow);
+                    if (two) tma_load_2d(sa + A_BYTES + BH_BYTES, m1, &ctl->full[s], kb * BKB, brow1);
                     for (int q = 0; q < boxes; ++q)
                         tma_load_2d(sa + q * 32 * BKB, &tmA, &ctl->full[s], kb * BKB, arow + 32 * q);
                     if (++s == S_STAGES) { s = 0; ph ^= 1u; }
@@ -817,6 +846,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             Unit w;
             for (int i = 0; !aborted && unit_at(un, b, i, w); ++i) {
                 const Tile t = tile_of(ctl, p, w.tile, BM);
+                const bool two = SWIGLU || t.n_blk * 256 + 128 < p.N;   // the tile has channels in its second half
                 const uint32_t id = idesc_i8(BM, (min(t.rows - t.m_blk * BM, BM) + 15) / 16 * 16);
                 if (!wait_i8(&ctl->tempty[acc], aph ^ 1u, ctl, p)) { aborted = true; break; }
                 tc_fence_after();
@@ -830,7 +860,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     for (int kk = 0; kk < BKB / 32; ++kk) {
                         const uint32_t accum = kb != w.kb0 || kk != 0 ? 1u : 0u;
                         mma_i8(d, w0 + 2u * kk, xd + 2u * kk, id, accum);
-                        mma_i8(d + 128u, w1 + 2u * kk, xd + 2u * kk, id, accum);
+                        if (two) mma_i8(d + 128u, w1 + 2u * kk, xd + 2u * kk, id, accum);
                     }
                     issued = true;
                     tc_commit(&ctl->empty[s]);
@@ -848,73 +878,104 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
     } else {
         const int q = warp & 3, r = q * 32 + lane;   // this thread's channel of each half
+        const int h = (warp - 2) >> 2;               // rows 16 h .. 16 h + 15 of every 32 are this warp's
+        float* my_sa = rows_sa + (warp - 2) * 64;
         int acc = 0;
         uint32_t aph = 0;
         OutT* out = static_cast<OutT*>(p.out);
-        Unit w;
-        for (int i = 0; unit_at(un, b, i, w); ++i) {
-            const Tile t = tile_of(ctl, p, w.tile, BM);
+        // What the epilogue needs of a unit, with its scales already on the
+        // way: fetched while the unit before it is finished.
+        struct Next {
+            Unit w;
+            Tile t;
+            bool some;
+            float f0, f1, s0, s1;
+        } nx;
+        auto fetch = [&](int i) {
+            nx.some = unit_at(un, b, i, nx.w);
+            if (!nx.some) return;
+            nx.t = tile_of(ctl, p, nx.w.tile, BM);
+            const int n0 = (SWIGLU ? nx.t.n_blk * 128 : nx.t.n_blk * 256) + r, n1 = SWIGLU ? n0 : n0 + 128;
+            const size_t sc = static_cast<size_t>(nx.t.g) * p.N;
+            nx.f0 = n0 < p.N ? p.sb0[sc + n0] : 0.f;
+            nx.f1 = n1 < p.N ? (SWIGLU ? p.sb1 : p.sb0)[sc + n1] : 0.f;
+            // lane l: the warp's rows l and 32 + l, which are rows (l / 16) 32 + 16 h + l % 16 of the tile, and 64 later
+            const int n = nx.t.rows - nx.t.m_blk * BM, c = (lane & 16) * 2 + 16 * h + (lane & 15);
+            const float* sap = p.sa + nx.t.row0 + static_cast<size_t>(nx.t.m_blk) * BM;
+            nx.s0 = c < min(n, BM) ? sap[c] : 0.f;
+            nx.s1 = c + 64 < min(n, BM) ? sap[c + 64] : 0.f;
+        };
+        fetch(0);
+        for (int i = 0; nx.some;) {
+            const Unit w = nx.w;
+            const Tile t = nx.t;
             int nrow = min(t.rows - t.m_blk * BM, BM);
             const size_t row0 = static_cast<size_t>(t.row0) + static_cast<size_t>(t.m_blk) * BM;
             const int ch0 = (SWIGLU ? t.n_blk * 128 : t.n_blk * 256) + r, ch1 = SWIGLU ? ch0 : ch0 + 128;
-            const size_t sc = static_cast<size_t>(t.g) * p.N;
-            const float f0 = ch0 < p.N ? p.sb0[sc + ch0] : 0.f;
-            const float f1 = ch1 < p.N ? (SWIGLU ? p.sb1 : p.sb0)[sc + ch1] : 0.f;
-            float sa_l[4];   // row scales: lane l holds rows l, 32 + l, 64 + l, 96 + l
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sa_l[j] = 32 * j + lane < nrow ? p.sa[row0 + 32 * j + lane] : 0.f;
+            const bool two = SWIGLU || t.n_blk * 256 + 128 < p.N;
+            const uint64_t f0 = pk(nx.f0, nx.f0), f1 = pk(nx.f1, nx.f1);
+            my_sa[lane] = nx.s0;
+            my_sa[32 + lane] = nx.s1;
+            __syncwarp();
+            fetch(++i);
             if (!wait_i8(&ctl->tfull[acc], aph, ctl, p)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * ACC_COLS);
             int* sums = p.part + static_cast<size_t>(w.tail) * 256 * p.part_rows + r;   // [row][256 channels]
             if (w.parts > 1) {
 #pragma unroll 1
-                for (int c = 0; c < nrow; c += 16) {
+                for (int c = 16 * h; c < nrow; c += 32) {
                     uint32_t lo[16], hi[16];
                     tmem_ld16x2(tb + c, tb + 128 + c, lo, hi);
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         if (c + j < nrow) {
                             red_add(sums + (c + j) * 256, lo[j]);
-                            red_add(sums + (c + j) * 256 + 128, hi[j]);
+                            if (two) red_add(sums + (c + j) * 256 + 128, hi[j]);
                         }
                 }
                 __threadfence();
                 __syncwarp();
                 int old = 0;
-                if (lane == 0) old = atomicAdd(p.sem + w.tail * 4 + q, 1);
+                if (lane == 0) old = atomicAdd(p.sem + w.tail * 8 + (warp - 2), 1);
                 old = __shfl_sync(0xffffffffu, old, 0);
                 __threadfence();
                 if (old != w.parts - 1) nrow = 0;   // another part comes later: its warp finishes
             }
-            {
 #pragma unroll 1
-                for (int c = 0; c < nrow; c += 16) {
-                    uint32_t lo[16], hi[16];
-                    if (w.parts == 1) {
-                        tmem_ld16x2(tb + c, tb + 128 + c, lo, hi);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            lo[j] = c + j < nrow ? static_cast<uint32_t>(__ldcg(sums + (c + j) * 256)) : 0u;
-                            hi[j] = c + j < nrow ? static_cast<uint32_t>(__ldcg(sums + (c + j) * 256 + 128)) : 0u;
-                        }
-                    }
-                    const float sa_c = c < 32 ? sa_l[0] : c < 64 ? sa_l[1] : c < 96 ? sa_l[2] : sa_l[3];
-                    OutT* o = out + (row0 + c) * p.N;
+            for (int c = 16 * h; c < nrow; c += 32) {
+                uint32_t lo[16], hi[16];
+                if (w.parts == 1) {
+                    tmem_ld16x2(tb + c, tb + 128 + c, lo, hi);
+                } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float sa = __shfl_sync(0xffffffffu, sa_c, (c & 16) + j);
-                        const bool in = c + j < nrow;
-                        const float y0 = scaled(lo[j], sa, f0), y1 = scaled(hi[j], sa, f1);
-                        if (SWIGLU) {
-                            if (in && ch0 < p.N) put(o + static_cast<size_t>(j) * p.N + ch0, swiglu(y0, y1, out));
-                        } else {
-                            if (in && ch0 < p.N) put(o + static_cast<size_t>(j) * p.N + ch0, y0);
-                            if (in && ch1 < p.N) put(o + static_cast<size_t>(j) * p.N + ch1, y1);
-                        }
+                        lo[j] = c + j < nrow ? static_cast<uint32_t>(__ldcg(sums + (c + j) * 256)) : 0u;
+                        hi[j] = two && c + j < nrow ? static_cast<uint32_t>(__ldcg(sums + (c + j) * 256 + 128)) : 0u;
                     }
                 }
+                const float* sap = my_sa + (c >> 5) * 16;
+                float y[SWIGLU ? 16 : 32];
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(sap + j);
+                    uint64_t a0 = scaled2(lo[j], lo[j + 1], s.x, f0), a1 = scaled2(lo[j + 2], lo[j + 3], s.y, f0);
+                    const uint64_t b0 = scaled2(hi[j], hi[j + 1], s.x, f1), b1 = scaled2(hi[j + 2], hi[j + 3], s.y, f1);
+                    if constexpr (SWIGLU) {
+                        a0 = swiglu2(a0, b0, out);
+                        a1 = swiglu2(a1, b1, out);
+                    } else {
+                        const float2 v0 = unpk(b0), v1 = unpk(b1);
+                        y[16 + j] = v0.x; y[17 + j] = v0.y; y[18 + j] = v1.x; y[19 + j] = v1.y;
+                    }
+                    const float2 u0 = unpk(a0), u1 = unpk(a1);
+                    y[j] = u0.x; y[j + 1] = u0.y; y[j + 2] = u1.x; y[j + 3] = u1.y;
+                }
+                OutT* o = out + (row0 + c) * p.N;
+                const int n = min(nrow - c, 16);
+                if (ch0 < p.N) put16(o + ch0, p.N, n, y);
+                if constexpr (!SWIGLU)
+                    if (ch1 < p.N) put16(o + ch1, p.N, n, y + 16);
             }
             tc_fence_before();
             __syncwarp();
@@ -953,7 +1014,7 @@ __global__ void __launch_bounds__(256) i8_begin_kernel(const KP p, int grid) {
         const int n = min(tile.rows - tile.m_blk * BM, BM) * 64;
         int4* part = reinterpret_cast<int4*>(p.part + static_cast<size_t>(t) * 256 * p.part_rows);
         for (int i = threadIdx.x; i < n; i += 256) part[i] = make_int4(0, 0, 0, 0);
-        if (threadIdx.x < 4) p.sem[t * 4 + threadIdx.x] = 0;
+        if (threadIdx.x < 8) p.sem[t * 8 + threadIdx.x] = 0;
     }
 }
 
@@ -982,9 +1043,12 @@ bool map_i8(CUtensorMap* m, const void* base, long long rows, int cols, int box_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A, B0, B1 and two more: pair A in boxes of 32 rows; single B0 and B1 in boxes of 64
+struct Maps {
+    CUtensorMap a, b0, b1, x0, x1;
+};
 template <auto KERNEL>
-cudaError_t launch_tc(size_t smem, int grid, int threads, const CUtensorMap& a, const CUtensorMap& b0,
-                      const CUtensorMap& b1, const CUtensorMap& a32, const KP& kp, cudaStream_t st) {
+cudaError_t launch_tc(size_t smem, int grid, const Maps& m, const KP& kp, cudaStream_t st) {
     static bool attr_set[64] = {};   // per kernel (template) and device; the size never changes
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -993,18 +1057,17 @@ cudaError_t launch_tc(size_t smem, int grid, int threads, const CUtensorMap& a, 
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    return launch_dep(KERNEL, dim3(grid), dim3(threads), smem, st, a, b0, b1, a32, kp);
+    return launch_dep(KERNEL, dim3(grid), dim3(NUM_THREADS), smem, st, m.a, m.b0, m.b1, m.x0, m.x1, kp);
 }
 
 template <bool SWIGLU, typename OutT>
-cudaError_t launch_form(const I8Gemm& g, const KP& kp, const CUtensorMap& a, const CUtensorMap& b0,
-                        const CUtensorMap& b1, const CUtensorMap& a32, cudaStream_t st) {
+cudaError_t launch_form(const I8Gemm& g, const KP& kp, const Maps& m, cudaStream_t st) {
     if (g.form == I8_PAIR)
         return launch_tc<i8_pair_kernel<SWIGLU, OutT>>(
                          P_STAGES * P_STAGE_BYTES + (P_XCH_FLOATS + P_SCALE_FLOATS) * 4 + 1024 + sizeof(Ctl<P_STAGES>),
-                         device_sm_count() & ~1, P_THREADS, a, b0, b1, a32, kp, st);
-    return launch_tc<i8_single_kernel<SWIGLU, OutT>>(S_STAGES * S_STAGE_BYTES + 1024 + sizeof(Ctl<S_STAGES>),
-                     std::min(device_sm_count(), kI8MaxGrid), NUM_THREADS, a, b0, b1, a32, kp, st);
+                         device_sm_count() & ~1, m, kp, st);
+    return launch_tc<i8_single_kernel<SWIGLU, OutT>>(S_STAGES * S_STAGE_BYTES + S_ROW_FLOATS * 4 + 1024 + sizeof(Ctl<S_STAGES>),
+                     std::min(device_sm_count(), kI8MaxGrid), m, kp, st);
 }
 
 }  // namespace
@@ -1012,13 +1075,21 @@ cudaError_t launch_form(const I8Gemm& g, const KP& kp, const CUtensorMap& a, con
 cudaError_t launch_i8_tc(const I8Gemm& g, cudaStream_t st) {
     const bool swiglu = g.B1 != nullptr, pair = g.form == I8_PAIR;
     const long long brows = static_cast<long long>(g.E) * g.N;
-    CUtensorMap a, b0, b1, a32;
-    const int bbox = pair ? 64 : 128;
-    if (!map_i8(&a, g.A, g.rows, g.K, pair ? BM : 32) || !map_i8(&b0, g.B0, brows, g.K, bbox)) return cudaErrorInvalidValue;
-    b1 = b0;
-    a32 = a;
-    if (pair && !map_i8(&a32, g.A, g.rows, g.K, 32)) return cudaErrorInvalidValue;
-    if (swiglu && !map_i8(&b1, g.B1, brows, g.K, bbox)) return cudaErrorInvalidValue;
+    Maps m;
+    const int box = pair ? 64 : 128;
+    bool ok = map_i8(&m.a, g.A, g.rows, g.K, pair ? BM : 32) && map_i8(&m.b0, g.B0, brows, g.K, box);
+    m.b1 = m.b0;
+    if (swiglu) ok = ok && map_i8(&m.b1, g.B1, brows, g.K, box);
+    if (pair) {
+        ok = ok && map_i8(&m.x0, g.A, g.rows, g.K, 32);
+        m.x1 = m.x0;
+    } else if (g.N % 128 != 0 && g.N % 128 <= 64) {
+        ok = ok && map_i8(&m.x0, g.B0, brows, g.K, 64) && map_i8(&m.x1, swiglu ? g.B1 : g.B0, brows, g.K, 64);
+    } else {   // no box of 64 rows
+        m.x0 = m.b0;
+        m.x1 = m.b1;
+    }
+    if (!ok) return cudaErrorInvalidValue;
     KP kp = {};
     kp.indptr = g.indptr; kp.sa = g.sa; kp.sb0 = g.sb0; kp.sb1 = g.sb1; kp.out = g.out; kp.status = g.status;
     kp.timeout_ns = wait_limit_ns();
@@ -1033,9 +1104,9 @@ cudaError_t launch_i8_tc(const I8Gemm& g, cudaStream_t st) {
     cudaError_t e = launch_dep(i8_begin_kernel, dim3(pair ? 1 : grid), dim3(256), 0, st, kp, grid);
     if (e != cudaSuccess) return e;
     if (g.out_dtype == MOE_DTYPE_BF16)
-        return swiglu ? launch_form<true, __nv_bfloat16>(g, kp, a, b0, b1, a32, st)
-                      : launch_form<false, __nv_bfloat16>(g, kp, a, b0, b1, a32, st);
-    return swiglu ? launch_form<true, float>(g, kp, a, b0, b1, a32, st) : launch_form<false, float>(g, kp, a, b0, b1, a32, st);
+        return swiglu ? launch_form<true, __nv_bfloat16>(g, kp, m, st)
+                      : launch_form<false, __nv_bfloat16>(g, kp, m, st);
+    return swiglu ? launch_form<true, float>(g, kp, m, st) : launch_form<false, float>(g, kp, m, st);
 }
 
 }  // namespace moe
