@@ -349,12 +349,13 @@ __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 6
 // channels).
 template <bool SWIGLU, typename OutT>
 __device__ __forceinline__ void whole_tile(const KP& p, const Item& it, uint32_t tb, int h, int r0, int ch0, float sa,
-                                           const float* sc, uint8_t* stage, OutT* out) {
+                                           const float* sc, uint8_t* stage, const CUtensorMap* om, OutT* out) {
     const int lane = threadIdx.x & 31;
     constexpr int HALF = SWIGLU ? 64 : 128;
     constexpr int RUN = 64 / sizeof(OutT);   // channels of a 64-byte run
     constexpr int PER = 16 / sizeof(OutT);   // channels of a piece
     const uint64_t sa2 = pk(sa, sa);
+    const bool whole = r0 + 32 <= it.n;   // all 32 rows are the tile's: one bulk store a run
 #pragma unroll 1
     for (int c = 0; c < HALF; c += 32) {
         uint32_t a[32], b[SWIGLU ? 32 : 1];
@@ -375,19 +376,31 @@ __device__ __forceinline__ void whole_tile(const KP& p, const Item& it, uint32_t
                 const float2 f0 = unpk(y0), f1 = unpk(y1);
                 v[i] = f0.x; v[i + 1] = f0.y; v[i + 2] = f1.x; v[i + 3] = f1.y;
             }
+            if (e % RUN == 0) {   // the run before has left the stage
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+            }
             stage16(stage, lane, (e / PER) & 3, v, out);
             if ((e + 16) % RUN == 0) {
-                __syncwarp();
-                const int ch = ch0 + HALF * h + c + e + 16 - RUN + (lane & 3) * PER;
-                if (ch < p.N) {   // N is a multiple of 16: pieces are in or out
+                const int ch = ch0 + HALF * h + c + e + 16 - RUN;   // N is a multiple of 16: pieces are in or out
+                if (whole) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && ch < p.N) tma_store_2d(om, smem_u32(stage), ch, static_cast<int>(it.row0) + r0);
+                    if (lane == 0) bulk_commit();
+                } else {
+                    __syncwarp();
+                    const int mine = ch + (lane & 3) * PER;
+                    if (mine < p.N) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = i * 8 + (lane >> 2);
-                        if (r0 + row < it.n)
-                            *reinterpret_cast<uint4*>(out + (it.row0 + r0 + row) * p.N + ch) = *stage_at(stage, row, lane & 3);
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = i * 8 + (lane >> 2);
+                            if (r0 + row < it.n)
+                                *reinterpret_cast<uint4*>(out + (it.row0 + r0 + row) * p.N + mine) = *stage_at(stage, row, lane & 3);
+                        }
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
     }
@@ -451,7 +464,7 @@ template <bool SWIGLU, typename OutT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmA32,
-               const __grid_constant__ CUtensorMap, const KP p) {
+               const __grid_constant__ CUtensorMap tmO, const KP p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* xch = reinterpret_cast<float*>(smem + P_STAGES * P_STAGE_BYTES);
@@ -625,43 +638,79 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         uint32_t tempty0[2] = {mapa_shared(smem_u32(&ctl->tempty[0]), 0u), mapa_shared(smem_u32(&ctl->tempty[1]), 0u)};
         OutT* out = static_cast<OutT*>(p.out);
         uint32_t aph[2] = {0u, 0u};
-        bool alive = true;
-        for (int u = cluster; u < work.items && alive; u += nclusters) {
-            const Item it = item_at(ctl, p, work, u);
-            if (it.n == 0) continue;
-            const int sets = sets_of(it);
-            const size_t gsb = static_cast<size_t>(it.t.g) * p.N;
-            for (int z = 0; z < sets; ++z) {
-                const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(z * ACC_COLS);
-                const int ch0 = it.t.n_blk * 2 * SET + z * SET;
-                // the scales of the epilogue are fetched before its wait
-                const int r = rank * BM + q * 32 + lane;
-                const float sa = !it.shrt && r < it.n ? p.sa[it.row0 + r] : 0.f;
-                if (!it.shrt) {
-                    __syncwarp();   // the warp has read the ones before
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const int ch = ch0 + (SWIGLU ? 64 * h + 32 * (v & 1) : 128 * h + 32 * v) + lane;
-                        scales[32 * v + lane] = ch < p.N ? (SWIGLU && v >= 2 ? p.sb1 : p.sb0)[gsb + ch] : 0.f;
+        // The set to come, with its scales already on the way: they are fetched
+        // while the set before is finished. 32 items are decoded at once, one a lane.
+        struct Next {
+            Item it;
+            int z, sets;
+            float sa, sc[4];
+        } nx;
+        Item mine;
+        int cnt = 0;
+        nx.z = nx.sets = 0;
+        auto fetch = [&]() {   // false past the last
+            if (++nx.z >= nx.sets) {
+                do {
+                    if ((cnt & 31) == 0) {
+                        const long long u = cluster + static_cast<long long>(cnt + lane) * nclusters;
+                        mine.n = -1;
+                        if (u < work.items) mine = item_at(ctl, p, work, static_cast<int>(u));
                     }
-                    __syncwarp();
-                }
-                const bool ok = wait_i8(&ctl->tfull[z], aph[z], ctl, p, peer_abort);
-                aph[z] ^= 1u;
-                // the warps of a pair leave together, so that neither waits for the other
-                if (SWIGLU ? !pair_and(pid, ok) : !ok) { alive = false; break; }
-                tc_fence_after();
-                if (!it.shrt) whole_tile<SWIGLU, OutT>(p, it, tb, h, r - lane, ch0, sa, scales, stage, out);
-                else if (SWIGLU) short_swiglu<OutT>(p, it, tb, h, gate, pid, xp, ch0 + rank * 64 + (q & 1) * 32 + lane, gsb, out);
-                else short_plain<OutT>(p, it, tb, h, ch0 + rank * 128 + q * 32 + lane, gsb, out);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (leader) mbar_arrive(&ctl->tempty[z]);
-                    else mbar_arrive_remote(tempty0[z]);
+                    const int from = cnt++ & 31;
+                    nx.it.n = __shfl_sync(0xffffffffu, mine.n, from);
+                    if (nx.it.n < 0) return false;
+                    nx.it.t.g = __shfl_sync(0xffffffffu, mine.t.g, from);
+                    nx.it.t.n_blk = __shfl_sync(0xffffffffu, mine.t.n_blk, from);
+                    nx.it.row0 = __shfl_sync(0xffffffffu, static_cast<int>(mine.row0), from);
+                } while (nx.it.n == 0);
+                nx.it.shrt = nx.it.n <= kShort;
+                nx.z = 0;
+                nx.sets = sets_of(nx.it);
+            }
+            if (!nx.it.shrt) {
+                const int r = rank * BM + q * 32 + lane, ch0 = nx.it.t.n_blk * 2 * SET + nx.z * SET;
+                const size_t gsb = static_cast<size_t>(nx.it.t.g) * p.N;
+                nx.sa = r < nx.it.n ? p.sa[nx.it.row0 + r] : 0.f;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int ch = ch0 + (SWIGLU ? 64 * h + 32 * (v & 1) : 128 * h + 32 * v) + lane;
+                    nx.sc[v] = ch < p.N ? (SWIGLU && v >= 2 ? p.sb1 : p.sb0)[gsb + ch] : 0.f;
                 }
             }
+            return true;
+        };
+        for (bool more = fetch(); more;) {
+            const Item it = nx.it;
+            const int z = nx.z, r0 = rank * BM + q * 32, ch0 = it.t.n_blk * 2 * SET + z * SET;
+            const size_t gsb = static_cast<size_t>(it.t.g) * p.N;
+            const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(z * ACC_COLS);
+            const float sa = nx.sa;
+            if (!it.shrt) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) scales[32 * v + lane] = nx.sc[v];
+                __syncwarp();
+            }
+            more = fetch();
+            const bool ok = wait_i8(&ctl->tfull[z], aph[z], ctl, p, peer_abort);
+            aph[z] ^= 1u;
+            // the warps of a pair leave together, so that neither waits for the other
+            if (SWIGLU ? !pair_and(pid, ok) : !ok) break;
+            tc_fence_after();
+            if (SWIGLU && it.shrt) {   // the stage is the trade's buffer too
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+            }
+            if (!it.shrt) whole_tile<SWIGLU, OutT>(p, it, tb, h, r0, ch0, sa, scales, stage, &tmO, out);
+            else if (SWIGLU) short_swiglu<OutT>(p, it, tb, h, gate, pid, xp, ch0 + rank * 64 + (q & 1) * 32 + lane, gsb, out);
+            else short_plain<OutT>(p, it, tb, h, ch0 + rank * 128 + q * 32 + lane, gsb, out);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(&ctl->tempty[z]);
+                else mbar_arrive_remote(tempty0[z]);
+            }
         }
+        if (lane == 0) bulk_wait_all();
     }
     tc_fence_before();
     cluster_sync_all();
@@ -1043,10 +1092,23 @@ bool map_i8(CUtensorMap* m, const void* base, long long rows, int cols, int box_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A, B0, B1 and two more: pair A in boxes of 32 rows; single B0 and B1 in boxes of 64
+// A, B0, B1 and two more: pair A in boxes of 32 rows and the results; single B0 and B1 in boxes of 64
 struct Maps {
     CUtensorMap a, b0, b1, x0, x1;
-};
+};// results [rows, N], boxes of 32 rows x 64 bytes in stage_at's order (64-byte swizzle)
+bool map_out(CUtensorMap* m, void* base, long long rows, int N, int dtype) {
+    const auto enc = encoder();
+    if (enc == nullptr) return false;
+    const bool bf = dtype == MOE_DTYPE_BF16;
+    const cuuint64_t es = bf ? 2 : 4;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(rows > 0 ? rows : 1)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(N) * es};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / es), 32}, estr[2] = {1, 1};
+    return enc(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <auto KERNEL>
 cudaError_t launch_tc(size_t smem, int grid, const Maps& m, const KP& kp, cudaStream_t st) {
     static bool attr_set[64] = {};   // per kernel (template) and device; the size never changes
@@ -1082,7 +1144,7 @@ cudaError_t launch_i8_tc(const I8Gemm& g, cudaStream_t st) {
     if (swiglu) ok = ok && map_i8(&m.b1, g.B1, brows, g.K, box);
     if (pair) {
         ok = ok && map_i8(&m.x0, g.A, g.rows, g.K, 32);
-        m.x1 = m.x0;
+        ok = ok && map_out(&m.x1, g.out, g.rows, g.N, g.out_dtype);
     } else if (g.N % 128 != 0 && g.N % 128 <= 64) {
         ok = ok && map_i8(&m.x0, g.B0, brows, g.K, 64) && map_i8(&m.x1, swiglu ? g.B1 : g.B0, brows, g.K, 64);
     } else {   // no box of 64 rows
