@@ -253,12 +253,20 @@ __device__ __forceinline__ uint64_t swiglu2(uint64_t a, uint64_t b, float* o) {
 __device__ __forceinline__ uint64_t scaled2(uint32_t s0, uint32_t s1, uint64_t sa, uint64_t sb) {
     return mul2(mul2(pk(static_cast<float>(static_cast<int>(s0)), static_cast<float>(static_cast<int>(s1))), sa), sb);
 }
-__device__ __forceinline__ float scaled(uint32_t s, float sa, float sb) {
-    return __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(s)), sa), sb);
-}
-
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+// the first n (at most CNT) of v, one under another
+template <int CNT, typename OutT>
+__device__ __forceinline__ void put_rows(OutT* o, int stride, int n, const float* v) {
+    if (n >= CNT) {
+#pragma unroll
+        for (int j = 0; j < CNT; ++j) put(o + static_cast<size_t>(j) * stride, v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < CNT - 1; ++j)
+            if (j < n) put(o + static_cast<size_t>(j) * stride, v[j]);
+    }
+}
 
 // Sixteen results as 16-byte pieces (bf16: 2, fp32: 4) to piece p0 of row `row` of a warp's 32 x 64-byte stage: piece
 // p lies at p ^ ((row / 2) % 4), so that eight lanes fall on different banks both here and when rows are read back.
@@ -300,7 +308,7 @@ __device__ __forceinline__ void stage16(uint8_t* st, int row, int p0, const floa
 // Eight warps share the epilogue, two to a quarter of the lanes.
 // The tiles that do not fill a whole wave run as two items of 128 rows each
 // when that still fits in one wave.
-constexpr int kShort = 192;
+constexpr int kShort = 192;   // at most: an epilogue warp holds 96 rows' scales
 struct Work {
     int full, items;
 };
@@ -405,58 +413,61 @@ __device__ __forceinline__ void whole_tile(const KP& p, const Item& it, uint32_t
         }
     }
 }
-// Short tile: a thread is channel ch, columns are rows of A.
+// Short tile: a thread is channel ch with scale f, columns are rows of A; sc:
+// the scales of the warp's rows, 32 of every 64, in shared memory.
 template <typename OutT>
-__device__ __forceinline__ void short_plain(const KP& p, const Item& it, uint32_t tb, int h, int ch, size_t gsb, OutT* out) {
-    const int lane = threadIdx.x & 31;
-    const float f = ch < p.N ? p.sb0[gsb + ch] : 0.f;
-    const float* sap = p.sa + it.row0;
+__device__ __forceinline__ void short_plain(const KP& p, const Item& it, uint32_t tb, int h, int ch, float f, const float* sc,
+                                            OutT* out) {
+    const uint64_t f2 = pk(f, f);
 #pragma unroll 1
-    for (int c = 32 * h; c < it.n; c += 64) {
-        const float sa_c = c + lane < it.n ? sap[c + lane] : 0.f;   // lane l: the scale of row c + l
+    for (int c = 32 * h; c < it.n; c += 64, sc += 32) {
         uint32_t v[32];
         tmem_ld32(tb + c, v);
-        OutT* o = out + (it.row0 + c) * p.N + ch;
+        float y[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float y = scaled(v[j], __shfl_sync(0xffffffffu, sa_c, j), f);
-            if (c + j < it.n && ch < p.N) put(o + static_cast<size_t>(j) * p.N, y);
+        for (int j = 0; j < 32; j += 4) {
+            const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(sc + j);
+            const float2 u0 = unpk(scaled2(v[j], v[j + 1], s.x, f2)), u1 = unpk(scaled2(v[j + 2], v[j + 3], s.y, f2));
+            y[j] = u0.x; y[j + 1] = u0.y; y[j + 2] = u1.x; y[j + 3] = u1.y;
         }
+        if (ch < p.N) put_rows<32>(out + (it.row0 + c) * p.N + ch, p.N, it.n - c, y);
     }
 }
 template <typename OutT>
 __device__ __forceinline__ void short_swiglu(const KP& p, const Item& it, uint32_t tb, int h, bool gate, int pid, float* xp,
-                                             int ch, size_t gsb, OutT* out) {
+                                             int ch, float f, const float* sc, OutT* out) {
     const int lane = threadIdx.x & 31;
-    const float f = ch < p.N ? (gate ? p.sb0 : p.sb1)[gsb + ch] : 0.f;
-    const float* sap = p.sa + it.row0;
+    const uint64_t f2 = pk(f, f);
     float* mine = xp + (gate ? 0 : 512);
     const float* other = xp + (gate ? 512 : 0);
 #pragma unroll 1
-    for (int c = 32 * h; c < it.n; c += 64) {
-        const float sa_c = c + lane < it.n ? sap[c + lane] : 0.f;
+    for (int c = 32 * h; c < it.n; c += 64, sc += 32) {
         uint32_t v[32];
         tmem_ld32(tb + c, v);
         float keep[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {   // rows 0..15 are the gate warp's to finish, 16..31 the up warp's
-            const float lo = scaled(v[j], __shfl_sync(0xffffffffu, sa_c, j), f);
-            const float hi = scaled(v[16 + j], __shfl_sync(0xffffffffu, sa_c, 16 + j), f);
-            keep[j] = gate ? lo : hi;
-            mine[j * 32 + lane] = gate ? hi : lo;
+        for (int j = 0; j < 16; j += 2) {   // rows 0..15 are the gate warp's to finish, 16..31 the up warp's
+            const float2 lo = unpk(scaled2(v[j], v[j + 1], *reinterpret_cast<const uint64_t*>(sc + j), f2));
+            const float2 hi = unpk(scaled2(v[16 + j], v[17 + j], *reinterpret_cast<const uint64_t*>(sc + 16 + j), f2));
+            keep[j] = gate ? lo.x : hi.x;
+            keep[j + 1] = gate ? lo.y : hi.y;
+            mine[j * 32 + lane] = gate ? hi.x : lo.x;
+            mine[(j + 1) * 32 + lane] = gate ? hi.y : lo.y;
         }
         pair_sync(pid);
-        const int c0 = c + (gate ? 0 : 16);
-        OutT* o = out + (it.row0 + c0) * p.N + ch;
-        float got[16];
+        float y[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) got[j] = other[j * 32 + lane];
+        for (int j = 0; j < 16; ++j) y[j] = other[j * 32 + lane];
         pair_sync(pid);   // both have read: the buffers are free
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float a = gate ? keep[j] : got[j], b = gate ? got[j] : keep[j];
-            if (c0 + j < it.n && ch < p.N) put(o + static_cast<size_t>(j) * p.N, swiglu(a, b, out));
+        for (int j = 0; j < 16; j += 2) {
+            const uint64_t k2 = pk(keep[j], keep[j + 1]), o2 = pk(y[j], y[j + 1]);
+            const float2 u = unpk(gate ? swiglu2(k2, o2, out) : swiglu2(o2, k2, out));
+            y[j] = u.x;
+            y[j + 1] = u.y;
         }
+        const int c0 = c + (gate ? 0 : 16);
+        if (ch < p.N) put_rows<16>(out + (it.row0 + c0) * p.N + ch, p.N, it.n - c0, y);
     }
 }
 
@@ -643,7 +654,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         struct Next {
             Item it;
             int z, sets;
-            float sa, sc[4];
+            float sa, sc[4] = {};
         } nx;
         Item mine;
         int cnt = 0;
@@ -667,10 +678,20 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 nx.z = 0;
                 nx.sets = sets_of(nx.it);
             }
-            if (!nx.it.shrt) {
-                const int r = rank * BM + q * 32 + lane, ch0 = nx.it.t.n_blk * 2 * SET + nx.z * SET;
-                const size_t gsb = static_cast<size_t>(nx.it.t.g) * p.N;
-                nx.sa = r < nx.it.n ? p.sa[nx.it.row0 + r] : 0.f;
+            const int ch0 = nx.it.t.n_blk * 2 * SET + nx.z * SET;
+            const size_t gsb = static_cast<size_t>(nx.it.t.g) * p.N;
+            const float* sap = p.sa + nx.it.row0;
+            if (nx.it.shrt) {   // sa: the thread's channel; sc: rows 32 h .. 32 h + 31 of every 64
+                const int ch = ch0 + lane + (SWIGLU ? rank * 64 + (q & 1) * 32 : rank * 128 + q * 32);
+                nx.sa = ch < p.N ? (SWIGLU && !gate ? p.sb1 : p.sb0)[gsb + ch] : 0.f;
+#pragma unroll
+                for (int v = 0; v < 3; ++v) {
+                    const int r = 64 * v + 32 * h + lane;
+                    nx.sc[v] = r < nx.it.n ? sap[r] : 0.f;
+                }
+            } else {            // sa: the thread's row; sc: the warp's channels
+                const int r = rank * BM + q * 32 + lane;
+                nx.sa = r < nx.it.n ? sap[r] : 0.f;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const int ch = ch0 + (SWIGLU ? 64 * h + 32 * (v & 1) : 128 * h + 32 * v) + lane;
@@ -682,14 +703,11 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         for (bool more = fetch(); more;) {
             const Item it = nx.it;
             const int z = nx.z, r0 = rank * BM + q * 32, ch0 = it.t.n_blk * 2 * SET + z * SET;
-            const size_t gsb = static_cast<size_t>(it.t.g) * p.N;
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(z * ACC_COLS);
             const float sa = nx.sa;
-            if (!it.shrt) {
 #pragma unroll
-                for (int v = 0; v < 4; ++v) scales[32 * v + lane] = nx.sc[v];
-                __syncwarp();
-            }
+            for (int v = 0; v < 4; ++v) scales[32 * v + lane] = nx.sc[v];
+            __syncwarp();
             more = fetch();
             const bool ok = wait_i8(&ctl->tfull[z], aph[z], ctl, p, peer_abort);
             aph[z] ^= 1u;
@@ -701,8 +719,8 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 __syncwarp();
             }
             if (!it.shrt) whole_tile<SWIGLU, OutT>(p, it, tb, h, r0, ch0, sa, scales, stage, &tmO, out);
-            else if (SWIGLU) short_swiglu<OutT>(p, it, tb, h, gate, pid, xp, ch0 + rank * 64 + (q & 1) * 32 + lane, gsb, out);
-            else short_plain<OutT>(p, it, tb, h, ch0 + rank * 128 + q * 32 + lane, gsb, out);
+            else if (SWIGLU) short_swiglu<OutT>(p, it, tb, h, gate, pid, xp, ch0 + rank * 64 + (q & 1) * 32 + lane, sa, scales, out);
+            else short_plain<OutT>(p, it, tb, h, ch0 + rank * 128 + q * 32 + lane, sa, scales, out);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -794,18 +812,6 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, uint32_t (
           "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
         : "r"(t0), "r"(t1)
         : "memory");
-}
-// v[0..n) one under another
-template <typename OutT>
-__device__ __forceinline__ void put16(OutT* o, int stride, int n, const float* v) {
-    if (n == 16) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) put(o + static_cast<size_t>(j) * stride, v[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 15; ++j)
-            if (j < n) put(o + static_cast<size_t>(j) * stride, v[j]);
-    }
 }
 __device__ __forceinline__ void red_add(int* p, uint32_t v) {
     asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
@@ -1021,10 +1027,10 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     y[j] = u0.x; y[j + 1] = u0.y; y[j + 2] = u1.x; y[j + 3] = u1.y;
                 }
                 OutT* o = out + (row0 + c) * p.N;
-                const int n = min(nrow - c, 16);
-                if (ch0 < p.N) put16(o + ch0, p.N, n, y);
+                const int n = nrow - c;
+                if (ch0 < p.N) put_rows<16>(o + ch0, p.N, n, y);
                 if constexpr (!SWIGLU)
-                    if (ch1 < p.N) put16(o + ch1, p.N, n, y + 16);
+                    if (ch1 < p.N) put_rows<16>(o + ch1, p.N, n, y + 16);
             }
             tc_fence_before();
             __syncwarp();
