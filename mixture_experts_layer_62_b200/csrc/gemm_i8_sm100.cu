@@ -8,8 +8,9 @@
 // as (float(sum) * sa) * sb and the result is rounded once.
 //
 // Two forms, both persistent kernels: one warp loads by TMA into a ring of
-// 128-byte K blocks (128-byte swizzle), one issues the MMAs, eight read the
-// accumulators back (tcgen05.ld), apply the scales and store, while the next tile runs into the other accumulator. The tile list
+// 128-byte K blocks (128-byte swizzle), one issues the MMAs, sixteen read the
+// accumulators back (tcgen05.ld), apply the scales and store: eight to each of
+// the two accumulators, which the tiles take in turn. The tile list
 // is formed in each CTA's shared memory from the group offsets. Every wait is
 // bounded (moe_set_wait_limit): on expiry the CTA records MOE_ERR_TIMEOUT,
 // lets what it started land, frees its tensor memory and returns.
@@ -46,11 +47,11 @@ constexpr int A_BYTES = BM * BKB;           // 16 KB
 constexpr int BH_BYTES = 128 * BKB;         // 128 weight rows, 16 KB
 constexpr int ACC_COLS = 256, TMEM_COLS = 512;
 constexpr int P_STAGES = 4, P_STAGE_BYTES = A_BYTES + 2 * BH_BYTES;
-constexpr int NUM_THREADS = 320;                    // eight epilogue warps
-constexpr int P_XCH_FLOATS = 4 * 2 * 16 * 32;       // pair SWIGLU: [warp pair][direction][16 rows][32 channels]
-constexpr int P_SCALE_FLOATS = 8 * 128;             // pair: the channel scales of each epilogue warp's columns
+constexpr int EPI = 16, NUM_THREADS = 64 + 32 * EPI;   // epilogue warps, threads
+constexpr int P_STAGE_FLOATS = 256;                 // pair: stage of an epilogue warp, or its half of a trade [8 rows][32 channels]
+constexpr int P_SCALE_FLOATS = 128;                 // pair: the scales of a warp's columns
 constexpr int S_STAGES = 4, S_STAGE_BYTES = A_BYTES + 2 * BH_BYTES;
-constexpr int S_ROW_FLOATS = 8 * 64;                // single: the row scales of each epilogue warp's columns
+constexpr int S_ROW_FLOATS = 64;                    // single: the row scales of a warp's columns
 constexpr long long kBandBytes = 32ll << 20;   // rows of A that a band of M blocks keeps in L2
 
 // kind::i8: A and B signed 8-bit, D signed 32-bit, both operands K-major
@@ -88,11 +89,11 @@ struct Ctl {
     uint32_t tmem_base;
     int abort_flag;
     int cum[MOE_MAX_E + 1];   // tiles before group g
-    int row0[MOE_MAX_E], nrow[MOE_MAX_E];
+    int row0[MOE_MAX_E + 1];  // first row of group g
 };
 
-// Tiles of every group in front of it, by one warp: cum[0..E], row0, nrow. A
-// group whose offsets do not fit in the rows is left out.
+// Tiles of every group in front of it, by one warp: cum[0..E], row0[0..E]. A
+// group whose offsets do not fit in the rows has none.
 template <int STAGES>
 __device__ __forceinline__ void list_tiles(Ctl<STAGES>* c, const KP& p, int tile_m) {
     const int lane = threadIdx.x & 31;
@@ -123,7 +124,7 @@ __device__ __forceinline__ void list_tiles(Ctl<STAGES>* c, const KP& p, int tile
             }
             if (g < p.E) {
                 c->row0[g] = lo[i];
-                c->nrow[g] = n;
+                if (g == p.E - 1) c->row0[p.E] = hi[i];
                 c->cum[g] = base + incl - v;
             }
             base += __shfl_sync(0xffffffffu, incl, 31);
@@ -147,8 +148,8 @@ __device__ __forceinline__ Tile tile_of(const Ctl<STAGES>* c, const KP& p, int i
     }
     Tile t;
     t.g = lo;
-    t.rows = c->nrow[lo];
     t.row0 = c->row0[lo];
+    t.rows = c->row0[lo + 1] - t.row0;
     id -= c->cum[lo];
     const int mt = (t.rows + tile_m - 1) / tile_m;
     int h = mt, m0 = 0;
@@ -227,8 +228,7 @@ constexpr float kNegLog2e = -1.4426950408889634f;
 // reciprocal (a few 2^-23 off, where the type rounds to 2^-8); fp32 results:
 // the accurate exponential, and the reciprocal of one unit in the last place
 // with subnormal results kept (a divide in its place took most of the
-// epilogue). exp(-a) overflowing gives a 0, as it should. The scalar and the
-// two-value form take the same roundings.
+// epilogue). exp(-a) overflowing gives a 0, as it should.
 __device__ __forceinline__ float rcp_full(float x) {
     float r;
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -236,9 +236,6 @@ __device__ __forceinline__ float rcp_full(float x) {
 }
 __device__ __forceinline__ float swiglu(float a, float b, float*) {
     return __fmul_rn(__fmul_rn(a, rcp_full(__fadd_rn(1.f, expf(-a)))), b);
-}
-__device__ __forceinline__ float swiglu(float a, float b, __nv_bfloat16*) {
-    return __fmul_rn(__fmul_rn(a, rcp(__fadd_rn(1.f, ex2(__fmul_rn(a, kNegLog2e))))), b);
 }
 __device__ __forceinline__ uint64_t swiglu2(uint64_t a, uint64_t b, __nv_bfloat16*) {
     const float2 t = unpk(mul2(a, pk(kNegLog2e, kNegLog2e)));
@@ -268,26 +265,49 @@ __device__ __forceinline__ void put_rows(OutT* o, int stride, int n, const float
     }
 }
 
-// Sixteen results as 16-byte pieces (bf16: 2, fp32: 4) to piece p0 of row `row` of a warp's 32 x 64-byte stage: piece
-// p lies at p ^ ((row / 2) % 4), so that eight lanes fall on different banks both here and when rows are read back.
+// Stage of a warp: 32 rows of 32 bytes, in the order of a 32-byte swizzle:
+// piece p (16 bytes) of a row lies at p ^ ((row / 4) % 2), so that eight lanes
+// fall on different banks both here and when rows are read back.
 __device__ __forceinline__ uint4* stage_at(uint8_t* st, int row, int p) {
-    return reinterpret_cast<uint4*>(st + row * 64 + ((p ^ ((row >> 1) & 3)) << 4));
+    return reinterpret_cast<uint4*>(st + row * 32 + ((p ^ ((row >> 2) & 1)) << 4));
 }
-__device__ __forceinline__ void stage16(uint8_t* st, int row, int, const float (&v)[16], float*) {
+__device__ __forceinline__ void stage_run(uint8_t* st, int row, const float* v, float*) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
         *stage_at(st, row, i) = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
                                            __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
 }
-__device__ __forceinline__ void stage16(uint8_t* st, int row, int p0, const float (&v)[16], __nv_bfloat16*) {
+__device__ __forceinline__ void stage_run(uint8_t* st, int row, const float* v, __nv_bfloat16*) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
         w[i] = *reinterpret_cast<uint32_t*>(&h);
     }
-    *stage_at(st, row, p0) = make_uint4(w[0], w[1], w[2], w[3]);
-    *stage_at(st, row, p0 + 1) = make_uint4(w[4], w[5], w[6], w[7]);
+    *stage_at(st, row, 0) = make_uint4(w[0], w[1], w[2], w[3]);
+    *stage_at(st, row, 1) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+// sixteen consecutive columns of this thread's TMEM lane, at one or two places
+__device__ __forceinline__ void tmem_ld16(uint32_t t0, uint32_t (&a)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
+          "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15])
+        : "r"(t0)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, uint32_t (&a)[16], uint32_t (&b)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
+          "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(b[0]),
+          "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]),
+          "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
+        : "r"(t0), "r"(t1)
+        : "memory");
 }
 
 // ---- pair form ----------------------------------------------------------------
@@ -308,7 +328,7 @@ __device__ __forceinline__ void stage16(uint8_t* st, int row, int p0, const floa
 // Eight warps share the epilogue, two to a quarter of the lanes.
 // The tiles that do not fill a whole wave run as two items of 128 rows each
 // when that still fits in one wave.
-constexpr int kShort = 192;   // at most: an epilogue warp holds 96 rows' scales
+constexpr int kShort = 192;   // at most 256: an epilogue warp holds the scales of half the rows
 struct Work {
     int full, items;
 };
@@ -360,55 +380,51 @@ __device__ __forceinline__ void whole_tile(const KP& p, const Item& it, uint32_t
                                            const float* sc, uint8_t* stage, const CUtensorMap* om, OutT* out) {
     const int lane = threadIdx.x & 31;
     constexpr int HALF = SWIGLU ? 64 : 128;
-    constexpr int RUN = 64 / sizeof(OutT);   // channels of a 64-byte run
+    constexpr int RUN = 32 / sizeof(OutT);   // channels of a run
     constexpr int PER = 16 / sizeof(OutT);   // channels of a piece
     const uint64_t sa2 = pk(sa, sa);
     const bool whole = r0 + 32 <= it.n;   // all 32 rows are the tile's: one bulk store a run
 #pragma unroll 1
-    for (int c = 0; c < HALF; c += 32) {
-        uint32_t a[32], b[SWIGLU ? 32 : 1];
-        tmem_ld32(tb + HALF * h + c, a);
-        if constexpr (SWIGLU) tmem_ld32(tb + 128 + HALF * h + c, b);
+    for (int c = 0; c < HALF; c += 16) {
+        uint32_t a[16], b[SWIGLU ? 16 : 1];
+        if constexpr (SWIGLU) tmem_ld16x2(tb + HALF * h + c, tb + 128 + HALF * h + c, a, b);
+        else tmem_ld16(tb + HALF * h + c, a);
+        float v[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 16) {
-            float v[16];
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const ulonglong2 s0 = *reinterpret_cast<const ulonglong2*>(sc + c + e + i);
-                uint64_t y0 = scaled2(a[e + i], a[e + i + 1], sa2, s0.x), y1 = scaled2(a[e + i + 2], a[e + i + 3], sa2, s0.y);
-                if constexpr (SWIGLU) {
-                    const ulonglong2 s1 = *reinterpret_cast<const ulonglong2*>(sc + 64 + c + e + i);
-                    y0 = swiglu2(y0, scaled2(b[e + i], b[e + i + 1], sa2, s1.x), out);
-                    y1 = swiglu2(y1, scaled2(b[e + i + 2], b[e + i + 3], sa2, s1.y), out);
-                }
-                const float2 f0 = unpk(y0), f1 = unpk(y1);
-                v[i] = f0.x; v[i + 1] = f0.y; v[i + 2] = f1.x; v[i + 3] = f1.y;
+        for (int i = 0; i < 16; i += 4) {
+            const ulonglong2 s0 = *reinterpret_cast<const ulonglong2*>(sc + c + i);
+            uint64_t y0 = scaled2(a[i], a[i + 1], sa2, s0.x), y1 = scaled2(a[i + 2], a[i + 3], sa2, s0.y);
+            if constexpr (SWIGLU) {
+                const ulonglong2 s1 = *reinterpret_cast<const ulonglong2*>(sc + 64 + c + i);
+                y0 = swiglu2(y0, scaled2(b[i], b[i + 1], sa2, s1.x), out);
+                y1 = swiglu2(y1, scaled2(b[i + 2], b[i + 3], sa2, s1.y), out);
             }
-            if (e % RUN == 0) {   // the run before has left the stage
-                if (lane == 0) bulk_wait_read<0>();
+            const float2 f0 = unpk(y0), f1 = unpk(y1);
+            v[i] = f0.x; v[i + 1] = f0.y; v[i + 2] = f1.x; v[i + 3] = f1.y;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += RUN) {
+            if (lane == 0) bulk_wait_read<0>();   // the run before has left the stage
+            __syncwarp();
+            stage_run(stage, lane, v + e, out);
+            const int ch = ch0 + HALF * h + c + e;   // N is a multiple of 16: runs are in or out
+            if (whole) {
+                fence_proxy_async_smem();
                 __syncwarp();
-            }
-            stage16(stage, lane, (e / PER) & 3, v, out);
-            if ((e + 16) % RUN == 0) {
-                const int ch = ch0 + HALF * h + c + e + 16 - RUN;   // N is a multiple of 16: pieces are in or out
-                if (whole) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && ch < p.N) tma_store_2d(om, smem_u32(stage), ch, static_cast<int>(it.row0) + r0);
-                    if (lane == 0) bulk_commit();
-                } else {
-                    __syncwarp();
-                    const int mine = ch + (lane & 3) * PER;
-                    if (mine < p.N) {
+                if (lane == 0 && ch < p.N) tma_store_2d(om, smem_u32(stage), ch, static_cast<int>(it.row0) + r0);
+                if (lane == 0) bulk_commit();
+            } else {
+                __syncwarp();
+                if (ch < p.N) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = i * 8 + (lane >> 2);
-                            if (r0 + row < it.n)
-                                *reinterpret_cast<uint4*>(out + (it.row0 + r0 + row) * p.N + mine) = *stage_at(stage, row, lane & 3);
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        const int row = i * 16 + (lane >> 1);
+                        if (r0 + row < it.n)
+                            *reinterpret_cast<uint4*>(out + (it.row0 + r0 + row) * p.N + ch + (lane & 1) * PER) =
+                                *stage_at(stage, row, lane & 1);
                     }
-                    __syncwarp();
                 }
+                __syncwarp();
             }
         }
     }
@@ -420,54 +436,55 @@ __device__ __forceinline__ void short_plain(const KP& p, const Item& it, uint32_
                                             OutT* out) {
     const uint64_t f2 = pk(f, f);
 #pragma unroll 1
-    for (int c = 32 * h; c < it.n; c += 64, sc += 32) {
-        uint32_t v[32];
-        tmem_ld32(tb + c, v);
-        float y[32];
+    for (int i = 0; i < kShort / 2; i += 16) {
+        const int c = 32 * h + (i & 16) + (i & ~31) * 2;
+        if (c >= it.n) continue;
+        uint32_t v[16];
+        tmem_ld16(tb + c, v);
+        float y[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(sc + j);
+        for (int j = 0; j < 16; j += 4) {
+            const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(sc + i + j);
             const float2 u0 = unpk(scaled2(v[j], v[j + 1], s.x, f2)), u1 = unpk(scaled2(v[j + 2], v[j + 3], s.y, f2));
             y[j] = u0.x; y[j + 1] = u0.y; y[j + 2] = u1.x; y[j + 3] = u1.y;
         }
-        if (ch < p.N) put_rows<32>(out + (it.row0 + c) * p.N + ch, p.N, it.n - c, y);
+        if (ch < p.N) put_rows<16>(out + (it.row0 + c) * p.N + ch, p.N, it.n - c, y);
     }
 }
 template <typename OutT>
-__device__ __forceinline__ void short_swiglu(const KP& p, const Item& it, uint32_t tb, int h, bool gate, int pid, float* xp,
-                                             int ch, float f, const float* sc, OutT* out) {
+__device__ __forceinline__ void short_swiglu(const KP& p, const Item& it, uint32_t tb, int h, bool gate, int pid, float* mine,
+                                             const float* other, int ch, float f, const float* sc, OutT* out) {
     const int lane = threadIdx.x & 31;
     const uint64_t f2 = pk(f, f);
-    float* mine = xp + (gate ? 0 : 512);
-    const float* other = xp + (gate ? 512 : 0);
 #pragma unroll 1
-    for (int c = 32 * h; c < it.n; c += 64, sc += 32) {
-        uint32_t v[32];
-        tmem_ld32(tb + c, v);
-        float keep[16];
+    for (int i = 0; i < kShort / 2; i += 16) {
+        const int c = 32 * h + (i & 16) + (i & ~31) * 2;
+        if (c >= it.n) continue;
+        uint32_t v[16];
+        tmem_ld16(tb + c, v);
+        float keep[8], y[8];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {   // rows 0..15 are the gate warp's to finish, 16..31 the up warp's
-            const float2 lo = unpk(scaled2(v[j], v[j + 1], *reinterpret_cast<const uint64_t*>(sc + j), f2));
-            const float2 hi = unpk(scaled2(v[16 + j], v[17 + j], *reinterpret_cast<const uint64_t*>(sc + 16 + j), f2));
+        for (int j = 0; j < 8; j += 2) {   // rows 0..7 are the gate warp's to finish, 8..15 the up warp's
+            const float2 lo = unpk(scaled2(v[j], v[j + 1], *reinterpret_cast<const uint64_t*>(sc + i + j), f2));
+            const float2 hi = unpk(scaled2(v[8 + j], v[9 + j], *reinterpret_cast<const uint64_t*>(sc + i + 8 + j), f2));
             keep[j] = gate ? lo.x : hi.x;
             keep[j + 1] = gate ? lo.y : hi.y;
             mine[j * 32 + lane] = gate ? hi.x : lo.x;
             mine[(j + 1) * 32 + lane] = gate ? hi.y : lo.y;
         }
         pair_sync(pid);
-        float y[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = other[j * 32 + lane];
+        for (int j = 0; j < 8; ++j) y[j] = other[j * 32 + lane];
         pair_sync(pid);   // both have read: the buffers are free
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
+        for (int j = 0; j < 8; j += 2) {
             const uint64_t k2 = pk(keep[j], keep[j + 1]), o2 = pk(y[j], y[j + 1]);
             const float2 u = unpk(gate ? swiglu2(k2, o2, out) : swiglu2(o2, k2, out));
             y[j] = u.x;
             y[j + 1] = u.y;
         }
-        const int c0 = c + (gate ? 0 : 16);
-        if (ch < p.N) put_rows<16>(out + (it.row0 + c0) * p.N + ch, p.N, it.n - c0, y);
+        const int c0 = c + (gate ? 0 : 8);
+        if (ch < p.N) put_rows<8>(out + (it.row0 + c0) * p.N + ch, p.N, it.n - c0, y);
     }
 }
 
@@ -480,7 +497,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* xch = reinterpret_cast<float*>(smem + P_STAGES * P_STAGE_BYTES);
     using C = Ctl<P_STAGES>;
-    C* ctl = reinterpret_cast<C*>(xch + P_XCH_FLOATS + P_SCALE_FLOATS);
+    C* ctl = reinterpret_cast<C*>(xch + EPI * (P_STAGE_FLOATS + P_SCALE_FLOATS));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     const bool leader = rank == 0;
@@ -494,7 +511,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&ctl->tfull[a], 1);
-            mbar_init(&ctl->tempty[a], 16);
+            mbar_init(&ctl->tempty[a], EPI);   // of both CTAs, half the epilogue warps each
         }
         mbar_init(&ctl->drain, 1);
         ctl->abort_flag = 0;
@@ -574,7 +591,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     } else if (warp == 1) {
         if (lane == 0 && leader) {
             int s = 0;
-            uint32_t ph = 0, aph[2] = {0u, 0u};
+            uint32_t ph = 0, aph[2] = {0u, 0u}, first_acc = 0;   // the accumulators take the sets in turn
             bool aborted = false, issued = false;
             for (int u = cluster; u < work.items && !aborted; u += nclusters) {
                 const Item it = item_at(ctl, p, work, u);
@@ -589,7 +606,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         const uint32_t sa = smem_u32(smem + st * P_STAGE_BYTES);
                         const uint64_t xd = sw128_desc(sa), wd = sw128_desc(sa + A_BYTES + z * BH_BYTES);
                         const uint64_t md = it.shrt ? wd : xd, nd = it.shrt ? xd : wd;
-                        const uint32_t d = tmem_base + static_cast<uint32_t>(z * ACC_COLS);
+                        const uint32_t d = tmem_base + ((first_acc + z) & 1u) * ACC_COLS;
 #pragma unroll
                         for (int kk = 0; kk < BKB / 32; ++kk)
                             mma_i8_pair(d, md + 2u * kk, nd + 2u * kk, id, (kb + i) | kk ? 1u : 0u);
@@ -599,13 +616,15 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                     return true;
                 };
+                auto full_acc = [&](int z) { tc_commit_pair_mc(&ctl->tfull[(first_acc + z) & 1u], 0x3); };
                 auto step = [&](int cnt) {
                     s += cnt;
                     if (s >= P_STAGES) { s -= P_STAGES; ph ^= 1u; }
                 };
                 auto free_acc = [&](int z) {
-                    const bool ok = wait_i8(&ctl->tempty[z], aph[z] ^ 1u, ctl, p, peer_abort);
-                    aph[z] ^= 1u;
+                    const uint32_t acc = (first_acc + z) & 1u;
+                    const bool ok = wait_i8(&ctl->tempty[acc], aph[acc] ^ 1u, ctl, p, peer_abort);
+                    aph[acc] ^= 1u;
                     tc_fence_after();
                     return ok;
                 };
@@ -614,7 +633,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 // complete while set 1 still runs.
                 const int first = min(P_STAGES, num_kb), last = sets == 2 ? min(P_STAGES, num_kb - first) : 0;
                 bool ok = free_acc(0) && run(0, first, 0, s, ph);
-                if (ok && first == num_kb) tc_commit_pair_mc(&ctl->tfull[0], 0x3);
+                if (ok && first == num_kb) full_acc(0);
                 if (ok && sets == 2) ok = free_acc(1) && run(0, first, 1, s, ph);
                 if (ok) step(first);
                 for (int kb = first; ok && kb < num_kb - last; ++kb) {
@@ -624,11 +643,12 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 }
                 if (ok && first < num_kb) {
                     ok = run(num_kb - last, last, 0, s, ph);
-                    if (ok) tc_commit_pair_mc(&ctl->tfull[0], 0x3);
+                    if (ok) full_acc(0);
                     if (ok && sets == 2) ok = run(num_kb - last, last, 1, s, ph);
                     if (ok) step(last);
                 }
-                if (ok && sets == 2) tc_commit_pair_mc(&ctl->tfull[1], 0x3);
+                if (ok && sets == 2) full_acc(1);
+                first_acc += sets;
                 aborted = !ok;
             }
             if (aborted && issued) {
@@ -639,17 +659,21 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     } else {
         const int q = warp & 3;
         const bool gate = q < 2;                      // short SWIGLU tiles: this warp's accumulators
-        const int h = (warp - 2) >> 2;                // which half of a set's columns
-        const int pid = 1 + (q & 1) + 2 * h;          // barrier of the warp pair
-        float* xp = xch + (pid - 1) * 2 * 512;
-        float* scales = xch + P_XCH_FLOATS + (warp - 2) * 128;
-        // whole tiles stage in the 2 KB in which the warp sends its half of a short one (read by the partner before
+        const int h = ((warp - 2) >> 2) & 1;          // which half of a set's columns
+        const int acc = (warp - 2) >> 3;              // which accumulator
+        const int pid = 1 + (q & 1) + 2 * h + 4 * acc;   // barrier of the warp pair
+        // whole tiles stage in the 1 KB in which the warp sends its half of a short one (read by the partner before
         // the barrier that ends every trade)
-        uint8_t* stage = reinterpret_cast<uint8_t*>(xp + (gate ? 0 : 512));
-        uint32_t tempty0[2] = {mapa_shared(smem_u32(&ctl->tempty[0]), 0u), mapa_shared(smem_u32(&ctl->tempty[1]), 0u)};
+        float* trade = xch + 2 * (pid - 1) * P_STAGE_FLOATS;
+        float* mine_st = trade + (gate ? 0 : P_STAGE_FLOATS);
+        const float* other_st = trade + (gate ? P_STAGE_FLOATS : 0);
+        uint8_t* stage = reinterpret_cast<uint8_t*>(mine_st);
+        float* scales = xch + EPI * P_STAGE_FLOATS + (warp - 2) * P_SCALE_FLOATS;
+        const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[acc]), 0u);
+        const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * ACC_COLS);
         OutT* out = static_cast<OutT*>(p.out);
-        uint32_t aph[2] = {0u, 0u};
-        // The set to come, with its scales already on the way: they are fetched
+        uint32_t aph = 0;
+        // This accumulator's set to come, with its scales already on the way: they are fetched
         // while the set before is finished. 32 items are decoded at once, one a lane.
         struct Next {
             Item it;
@@ -657,27 +681,29 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             float sa, sc[4] = {};
         } nx;
         Item mine;
-        int cnt = 0;
+        int cnt = 0, seen = 0;   // items and sets so far
         nx.z = nx.sets = 0;
         auto fetch = [&]() {   // false past the last
-            if (++nx.z >= nx.sets) {
-                do {
-                    if ((cnt & 31) == 0) {
-                        const long long u = cluster + static_cast<long long>(cnt + lane) * nclusters;
-                        mine.n = -1;
-                        if (u < work.items) mine = item_at(ctl, p, work, static_cast<int>(u));
-                    }
-                    const int from = cnt++ & 31;
-                    nx.it.n = __shfl_sync(0xffffffffu, mine.n, from);
-                    if (nx.it.n < 0) return false;
-                    nx.it.t.g = __shfl_sync(0xffffffffu, mine.t.g, from);
-                    nx.it.t.n_blk = __shfl_sync(0xffffffffu, mine.t.n_blk, from);
-                    nx.it.row0 = __shfl_sync(0xffffffffu, static_cast<int>(mine.row0), from);
-                } while (nx.it.n == 0);
-                nx.it.shrt = nx.it.n <= kShort;
-                nx.z = 0;
-                nx.sets = sets_of(nx.it);
-            }
+            do {
+                if (++nx.z >= nx.sets) {
+                    do {
+                        if ((cnt & 31) == 0) {
+                            const long long u = cluster + static_cast<long long>(cnt + lane) * nclusters;
+                            mine.n = -1;
+                            if (u < work.items) mine = item_at(ctl, p, work, static_cast<int>(u));
+                        }
+                        const int from = cnt++ & 31;
+                        nx.it.n = __shfl_sync(0xffffffffu, mine.n, from);
+                        if (nx.it.n < 0) return false;
+                        nx.it.t.g = __shfl_sync(0xffffffffu, mine.t.g, from);
+                        nx.it.t.n_blk = __shfl_sync(0xffffffffu, mine.t.n_blk, from);
+                        nx.it.row0 = __shfl_sync(0xffffffffu, static_cast<int>(mine.row0), from);
+                    } while (nx.it.n == 0);
+                    nx.it.shrt = nx.it.n <= kShort;
+                    nx.z = 0;
+                    nx.sets = sets_of(nx.it);
+                }
+            } while ((seen++ & 1) != acc);
             const int ch0 = nx.it.t.n_blk * 2 * SET + nx.z * SET;
             const size_t gsb = static_cast<size_t>(nx.it.t.g) * p.N;
             const float* sap = p.sa + nx.it.row0;
@@ -700,34 +726,41 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
             return true;
         };
+        bool met = false;
         for (bool more = fetch(); more;) {
             const Item it = nx.it;
-            const int z = nx.z, r0 = rank * BM + q * 32, ch0 = it.t.n_blk * 2 * SET + z * SET;
-            const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(z * ACC_COLS);
+            const int r0 = rank * BM + q * 32, ch0 = it.t.n_blk * 2 * SET + nx.z * SET;
             const float sa = nx.sa;
 #pragma unroll
             for (int v = 0; v < 4; ++v) scales[32 * v + lane] = nx.sc[v];
             __syncwarp();
             more = fetch();
-            const bool ok = wait_i8(&ctl->tfull[z], aph[z], ctl, p, peer_abort);
-            aph[z] ^= 1u;
-            // the warps of a pair leave together, so that neither waits for the other
-            if (SWIGLU ? !pair_and(pid, ok) : !ok) break;
+            const bool ok = wait_i8(&ctl->tfull[acc], aph, ctl, p, peer_abort);
+            aph ^= 1u;
+            // The warps of a pair leave together, so that neither waits for the other: on the word of both at a
+            // short tile, else after the loop, where one that has left early answers the other's last question.
+            if (SWIGLU && it.shrt) {
+                met = !pair_and(pid, ok);
+                if (met) break;
+            } else if (!ok) {
+                break;
+            }
             tc_fence_after();
             if (SWIGLU && it.shrt) {   // the stage is the trade's buffer too
                 if (lane == 0) bulk_wait_read<0>();
                 __syncwarp();
             }
             if (!it.shrt) whole_tile<SWIGLU, OutT>(p, it, tb, h, r0, ch0, sa, scales, stage, &tmO, out);
-            else if (SWIGLU) short_swiglu<OutT>(p, it, tb, h, gate, pid, xp, ch0 + rank * 64 + (q & 1) * 32 + lane, sa, scales, out);
+            else if (SWIGLU) short_swiglu<OutT>(p, it, tb, h, gate, pid, mine_st, other_st, ch0 + rank * 64 + (q & 1) * 32 + lane, sa, scales, out);
             else short_plain<OutT>(p, it, tb, h, ch0 + rank * 128 + q * 32 + lane, sa, scales, out);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (leader) mbar_arrive(&ctl->tempty[z]);
-                else mbar_arrive_remote(tempty0[z]);
+                if (leader) mbar_arrive(&ctl->tempty[acc]);
+                else mbar_arrive_remote(tempty0);
             }
         }
+        if (SWIGLU && !met) pair_and(pid, false);
         if (lane == 0) bulk_wait_all();
     }
     tc_fence_before();
@@ -800,19 +833,6 @@ __device__ __forceinline__ bool unit_at(const Units& u, int b, int i, Unit& o) {
     return true;
 }
 
-// sixteen consecutive columns of this thread's TMEM lane, at two places
-__device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, uint32_t (&a)[16], uint32_t (&b)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
-          "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(b[0]),
-          "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]),
-          "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
-        : "r"(t0), "r"(t1)
-        : "memory");
-}
 __device__ __forceinline__ void red_add(int* p, uint32_t v) {
     asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
@@ -826,7 +846,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     using C = Ctl<S_STAGES>;
     float* rows_sa = reinterpret_cast<float*>(smem + S_STAGES * S_STAGE_BYTES);
-    C* ctl = reinterpret_cast<C*>(rows_sa + S_ROW_FLOATS);
+    C* ctl = reinterpret_cast<C*>(rows_sa + EPI * S_ROW_FLOATS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = static_cast<int>(blockIdx.x);
 
@@ -837,7 +857,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&ctl->tfull[a], 1);
-            mbar_init(&ctl->tempty[a], 8);
+            mbar_init(&ctl->tempty[a], EPI / 2);
         }
         mbar_init(&ctl->drain, 1);
         ctl->abort_flag = 0;
@@ -933,9 +953,9 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
     } else {
         const int q = warp & 3, r = q * 32 + lane;   // this thread's channel of each half
-        const int h = (warp - 2) >> 2;               // rows 16 h .. 16 h + 15 of every 32 are this warp's
-        float* my_sa = rows_sa + (warp - 2) * 64;
-        int acc = 0;
+        const int h = ((warp - 2) >> 2) & 1;         // rows 16 h .. 16 h + 15 of every 32 are this warp's
+        const int acc = (warp - 2) >> 3;             // units acc, acc + 2, .. are its accumulator's
+        float* my_sa = rows_sa + (warp - 2) * S_ROW_FLOATS;
         uint32_t aph = 0;
         OutT* out = static_cast<OutT*>(p.out);
         // What the epilogue needs of a unit, with its scales already on the
@@ -954,14 +974,14 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const size_t sc = static_cast<size_t>(nx.t.g) * p.N;
             nx.f0 = n0 < p.N ? p.sb0[sc + n0] : 0.f;
             nx.f1 = n1 < p.N ? (SWIGLU ? p.sb1 : p.sb0)[sc + n1] : 0.f;
-            // lane l: the warp's rows l and 32 + l, which are rows (l / 16) 32 + 16 h + l % 16 of the tile, and 64 later
+            // lane l: the l-th and the (l + 32)-th of the warp's rows
             const int n = nx.t.rows - nx.t.m_blk * BM, c = (lane & 16) * 2 + 16 * h + (lane & 15);
             const float* sap = p.sa + nx.t.row0 + static_cast<size_t>(nx.t.m_blk) * BM;
             nx.s0 = c < min(n, BM) ? sap[c] : 0.f;
             nx.s1 = c + 64 < min(n, BM) ? sap[c + 64] : 0.f;
         };
-        fetch(0);
-        for (int i = 0; nx.some;) {
+        fetch(acc);
+        for (int i = acc; nx.some;) {
             const Unit w = nx.w;
             const Tile t = nx.t;
             int nrow = min(t.rows - t.m_blk * BM, BM);
@@ -972,7 +992,8 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             my_sa[lane] = nx.s0;
             my_sa[32 + lane] = nx.s1;
             __syncwarp();
-            fetch(++i);
+            i += 2;
+            fetch(i);
             if (!wait_i8(&ctl->tfull[acc], aph, ctl, p)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * ACC_COLS);
@@ -992,7 +1013,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 __threadfence();
                 __syncwarp();
                 int old = 0;
-                if (lane == 0) old = atomicAdd(p.sem + w.tail * 8 + (warp - 2), 1);
+                if (lane == 0) old = atomicAdd(p.sem + w.tail * 8 + 4 * h + q, 1);
                 old = __shfl_sync(0xffffffffu, old, 0);
                 __threadfence();
                 if (old != w.parts - 1) nrow = 0;   // another part comes later: its warp finishes
@@ -1035,8 +1056,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->tempty[acc]);
-            acc ^= 1;
-            if (acc == 0) aph ^= 1u;
+            aph ^= 1u;
         }
     }
     tc_fence_before();
@@ -1101,7 +1121,7 @@ bool map_i8(CUtensorMap* m, const void* base, long long rows, int cols, int box_
 // A, B0, B1 and two more: pair A in boxes of 32 rows and the results; single B0 and B1 in boxes of 64
 struct Maps {
     CUtensorMap a, b0, b1, x0, x1;
-};// results [rows, N], boxes of 32 rows x 64 bytes in stage_at's order (64-byte swizzle)
+};// results [rows, N], boxes of 32 rows x 32 bytes in stage_at's order (32-byte swizzle)
 bool map_out(CUtensorMap* m, void* base, long long rows, int N, int dtype) {
     const auto enc = encoder();
     if (enc == nullptr) return false;
@@ -1109,9 +1129,9 @@ bool map_out(CUtensorMap* m, void* base, long long rows, int N, int dtype) {
     const cuuint64_t es = bf ? 2 : 4;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(rows > 0 ? rows : 1)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(N) * es};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / es), 32}, estr[2] = {1, 1};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(32 / es), 32}, estr[2] = {1, 1};
     return enc(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1132,9 +1152,9 @@ template <bool SWIGLU, typename OutT>
 cudaError_t launch_form(const I8Gemm& g, const KP& kp, const Maps& m, cudaStream_t st) {
     if (g.form == I8_PAIR)
         return launch_tc<i8_pair_kernel<SWIGLU, OutT>>(
-                         P_STAGES * P_STAGE_BYTES + (P_XCH_FLOATS + P_SCALE_FLOATS) * 4 + 1024 + sizeof(Ctl<P_STAGES>),
+                         P_STAGES * P_STAGE_BYTES + EPI * (P_STAGE_FLOATS + P_SCALE_FLOATS) * 4 + 1024 + sizeof(Ctl<P_STAGES>),
                          device_sm_count() & ~1, m, kp, st);
-    return launch_tc<i8_single_kernel<SWIGLU, OutT>>(S_STAGES * S_STAGE_BYTES + S_ROW_FLOATS * 4 + 1024 + sizeof(Ctl<S_STAGES>),
+    return launch_tc<i8_single_kernel<SWIGLU, OutT>>(S_STAGES * S_STAGE_BYTES + EPI * S_ROW_FLOATS * 4 + 1024 + sizeof(Ctl<S_STAGES>),
                      std::min(device_sm_count(), kI8MaxGrid), m, kp, st);
 }
 
