@@ -90,6 +90,7 @@ struct Ctl {
     int abort_flag;
     int cum[MOE_MAX_E + 1];   // tiles before group g
     int row0[MOE_MAX_E + 1];  // first row of group g
+    int most;                 // rows of the tallest tile
 };
 
 // Tiles of every group in front of it, by one warp: cum[0..E], row0[0..E]. A
@@ -97,7 +98,7 @@ struct Ctl {
 template <int STAGES>
 __device__ __forceinline__ void list_tiles(Ctl<STAGES>* c, const KP& p, int tile_m) {
     const int lane = threadIdx.x & 31;
-    int base = 0;
+    int base = 0, most = 0;
     bool bad = false;
     // eight times 32 groups' offsets requested at once: one memory round trip up to 256 experts
     for (int b0 = 0; b0 < p.E; b0 += 256) {
@@ -115,6 +116,7 @@ __device__ __forceinline__ void list_tiles(Ctl<STAGES>* c, const KP& p, int tile
             const bool ok = lo[i] >= 0 && hi[i] >= lo[i] && hi[i] <= p.rows;
             const int n = ok ? hi[i] - lo[i] : 0;
             bad |= !ok;
+            most = max(most, n);
             const int v = (n + tile_m - 1) / tile_m * p.nt;
             int incl = v;
 #pragma unroll
@@ -130,7 +132,11 @@ __device__ __forceinline__ void list_tiles(Ctl<STAGES>* c, const KP& p, int tile
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
-    if (lane == 0) c->cum[p.E] = base;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+        c->cum[p.E] = base;
+        c->most = min(most, tile_m);
+    }
     if (kDebugChecks && __any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) debug_record_bounds(p.status);
 }
 
@@ -801,15 +807,25 @@ struct Units {
         return static_cast<int>((static_cast<long long>(r + 1) * n - 1) / (static_cast<long long>(tail) * nkb));
     }
 };
-constexpr int kMinShare = 4;   // K blocks: shorter shares cost more in joining than they save
-__device__ __forceinline__ Units units_of(int tiles, int nkb, int grid) {
+// Whether the tail is cut: shares of kMinShare K blocks or more, one to a CTA,
+// if that shortens the tail by more K blocks than joining costs. Joining is
+// two passes over each part's sums in L2 and the zeros before: about as long
+// as 4 K blocks and one for every 10 rows of the tallest tile. Measured cut /
+// not cut: 46 rows of K = 11264 (down, 8 experts, N = 4096) 85 / 85 us and with 2
+// experts of one row 34 / 50; 128 rows, K = 1408, 96 tiles 27 / 16; 128 rows, K =
+// 8400, 20 tiles 48 / 62; 36 rows, K = 1792, 76 tiles in the tail 34 / 22.
+constexpr int kMinShare = 4;
+__device__ __forceinline__ Units units_of(int tiles, int most, int nkb, int grid) {
     Units u;
     u.grid = grid;
     u.nkb = nkb;
     u.whole = tiles / grid;
     u.tail = tiles - u.whole * grid;
-    const int shares = static_cast<int>((static_cast<long long>(u.tail) * nkb + kMinShare - 1) / kMinShare);
-    u.n = max(min(grid, max(shares, u.tail)), 1);
+    const long long blocks = static_cast<long long>(u.tail) * nkb;
+    const int shares = static_cast<int>(min((blocks + kMinShare - 1) / kMinShare, static_cast<long long>(grid)));
+    u.n = max(shares, max(u.tail, 1));
+    const int share = static_cast<int>((blocks + u.n - 1) / u.n);
+    if (nkb - share <= 4 + most / 10) u.n = max(u.tail, 1);
     return u;
 }
 // Unit i of CTA b; false past the last.
@@ -875,7 +891,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = ctl->tmem_base;
-    const Units un = units_of(ctl->cum[p.E], (p.K + BKB - 1) / BKB, static_cast<int>(gridDim.x));
+    const Units un = units_of(ctl->cum[p.E], ctl->most, (p.K + BKB - 1) / BKB, static_cast<int>(gridDim.x));
 
     if (warp == 0) {
         if (lane == 0) {
@@ -1082,7 +1098,7 @@ __global__ void __launch_bounds__(256) i8_begin_kernel(const KP p, int grid) {
     if (p.part == nullptr) return;
     if (threadIdx.x < 32) list_tiles(&c, p, BM);
     __syncthreads();
-    const Units u = units_of(c.cum[p.E], (p.K + BKB - 1) / BKB, grid);
+    const Units u = units_of(c.cum[p.E], c.most, (p.K + BKB - 1) / BKB, grid);
     if (u.n <= u.tail) return;   // no tile has more than one part
     for (int t = blockIdx.x; t < u.tail; t += gridDim.x) {
         const Tile tile = tile_of(&c, p, u.whole * u.grid + t, BM);
