@@ -8,11 +8,11 @@
 // as (float(sum) * sa) * sb and the result is rounded once.
 //
 // Two forms, both persistent kernels: one warp loads by TMA into a ring of
-// 128-byte K blocks (128-byte swizzle), one issues the MMAs, sixteen read the
-// accumulators back (tcgen05.ld), apply the scales and store: eight to each of
-// the two accumulators, which the tiles take in turn. The tile list
-// is formed in each CTA's shared memory from the group offsets. Every wait is
-// bounded (moe_set_wait_limit): on expiry the CTA records MOE_ERR_TIMEOUT,
+// 128-byte K blocks (128-byte swizzle), one issues the MMAs, sixteen (or eight)
+// read the accumulators back (tcgen05.ld), apply the scales and store: half of
+// them to each of the two accumulators, which the tiles take in turn. The tile
+// list is formed in each CTA's shared memory from the group offsets. Every wait
+// is bounded (moe_set_wait_limit): on expiry the CTA records MOE_ERR_TIMEOUT,
 // lets what it started land, frees its tensor memory and returns.
 //  * pair: clusters of two CTAs share tiles of 256 rows of A x 512 weight
 //    rows (cta_group::2), each CTA loading half of both; groups of many rows.
@@ -233,8 +233,8 @@ constexpr float kNegLog2e = -1.4426950408889634f;
 // SiLU(a) b = (a / (1 + exp(-a))) b. bf16 results: the fast exponential and
 // reciprocal (a few 2^-23 off, where the type rounds to 2^-8); fp32 results:
 // the accurate exponential, and the reciprocal of one unit in the last place
-// with subnormal results kept (a divide in its place took most of the
-// epilogue). exp(-a) overflowing gives a 0, as it should.
+// with subnormal results kept (a divide in its place: 156 us where this takes
+// 100; 3000 rows, K = 64, 11328 channels). exp(-a) overflowing gives a 0, as it should.
 __device__ __forceinline__ float rcp_full(float x) {
     float r;
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -331,7 +331,10 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, uint32_t (
 // channels. (That trade is why whole tiles are not laid out this way too: it
 // made the up projection of 8192 rows take 731 us instead of 710.) kShort
 // between 64 and 192 measures the same within 2 %, 255 costs 3 to 5 %.
-// Eight warps share the epilogue, two to a quarter of the lanes.
+// Eight warps share an accumulator's epilogue, two to a quarter of the lanes.
+// The other accumulator's eight run beside them: with K = 64, where nothing but
+// the epilogue takes time, that gave 435 us where the same eight for both took
+// 540 and sixteen for each in turn 493.
 // The tiles that do not fill a whole wave run as two items of 128 rows each
 // when that still fits in one wave.
 constexpr int kShort = 192;   // at most 256: an epilogue warp holds the scales of half the rows
@@ -377,10 +380,13 @@ __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 6
 // Epilogues of one set by one warp (half h of its columns).
 // Whole tile: a thread is row r, columns are channels from ch0.
 // sc: the scales of the warp's columns in shared memory (SWIGLU 64 of B0,
-// then 64 of B1). The results go through a 2 KB stage of the warp, so that
-// every row is written in whole 64-byte runs: with each lane storing its own
-// row's 16 bytes the stores alone cost 36 of 435 us (4096 rows, K = 4096, 18944
-// channels).
+// then 64 of B1). The results go through a 1 KB stage of the warp and leave as
+// bulk tensor stores of 32 rows x 32 bytes, which nothing waits for but the
+// next use of the stage; the last rows of a group by plain 16-byte stores of
+// the same runs. With each lane storing its own row's 16 bytes the stores
+// alone cost 36 of 435 us (4096 rows, K = 4096, 18944 channels); staged plain
+// stores took 309 us where bulk stores take 304 (8192 rows, K = 14336) and 608
+// where they take 540 (33474 rows, K = 64, 11328 channels).
 template <bool SWIGLU, typename OutT>
 __device__ __forceinline__ void whole_tile(const KP& p, const Item& it, uint32_t tb, int h, int r0, int ch0, float sa,
                                            const float* sc, uint8_t* stage, const CUtensorMap* om, OutT* out) {
@@ -785,7 +791,8 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 // B0) against up to 128 rows of A as N = 16, 32, .. 128, so a group of few
 // rows costs few tensor cycles and few bytes beside its weights, and a
 // thread of the epilogue owns a channel: its two scales are loaded once and
-// every store of a warp is 32 consecutive channels of one row.
+// every store of a warp is 32 consecutive channels of one row. H warps share a
+// quarter of the channels of an accumulator, 16 rows of every 16 H each.
 //
 // Units: the tiles that fill whole waves of the grid run one to a CTA, in
 // order, over all of K. The tail tiles are cut along K into equal shares for
@@ -853,8 +860,8 @@ __device__ __forceinline__ void red_add(int* p, uint32_t v) {
     asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-template <bool SWIGLU, typename OutT>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+template <bool SWIGLU, typename OutT, int H>
+__global__ void __launch_bounds__(64 + 256 * H, 1)
 i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                  const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmB0h,
                  const __grid_constant__ CUtensorMap tmB1h, const KP p) {
@@ -862,7 +869,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     using C = Ctl<S_STAGES>;
     float* rows_sa = reinterpret_cast<float*>(smem + S_STAGES * S_STAGE_BYTES);
-    C* ctl = reinterpret_cast<C*>(rows_sa + EPI * S_ROW_FLOATS);
+    C* ctl = reinterpret_cast<C*>(rows_sa + 8 * H * S_ROW_FLOATS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = static_cast<int>(blockIdx.x);
 
@@ -873,7 +880,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&ctl->tfull[a], 1);
-            mbar_init(&ctl->tempty[a], EPI / 2);
+            mbar_init(&ctl->tempty[a], 4 * H);
         }
         mbar_init(&ctl->drain, 1);
         ctl->abort_flag = 0;
@@ -969,8 +976,8 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
     } else {
         const int q = warp & 3, r = q * 32 + lane;   // this thread's channel of each half
-        const int h = ((warp - 2) >> 2) & 1;         // rows 16 h .. 16 h + 15 of every 32 are this warp's
-        const int acc = (warp - 2) >> 3;             // units acc, acc + 2, .. are its accumulator's
+        const int h = ((warp - 2) >> 2) % H;         // rows 16 h .. 16 h + 15 of every 16 H are this warp's
+        const int acc = (warp - 2) / (4 * H);        // units acc, acc + 2, .. are its accumulator's
         float* my_sa = rows_sa + (warp - 2) * S_ROW_FLOATS;
         uint32_t aph = 0;
         OutT* out = static_cast<OutT*>(p.out);
@@ -991,10 +998,10 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             nx.f0 = n0 < p.N ? p.sb0[sc + n0] : 0.f;
             nx.f1 = n1 < p.N ? (SWIGLU ? p.sb1 : p.sb0)[sc + n1] : 0.f;
             // lane l: the l-th and the (l + 32)-th of the warp's rows
-            const int n = nx.t.rows - nx.t.m_blk * BM, c = (lane & 16) * 2 + 16 * h + (lane & 15);
+            const int n = nx.t.rows - nx.t.m_blk * BM, c = (lane & 16) * H + 16 * h + (lane & 15);
             const float* sap = p.sa + nx.t.row0 + static_cast<size_t>(nx.t.m_blk) * BM;
             nx.s0 = c < min(n, BM) ? sap[c] : 0.f;
-            nx.s1 = c + 64 < min(n, BM) ? sap[c + 64] : 0.f;
+            nx.s1 = c + 32 * H < min(n, BM) ? sap[c + 32 * H] : 0.f;
         };
         fetch(acc);
         for (int i = acc; nx.some;) {
@@ -1016,7 +1023,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             int* sums = p.part + static_cast<size_t>(w.tail) * 256 * p.part_rows + r;   // [row][256 channels]
             if (w.parts > 1) {
 #pragma unroll 1
-                for (int c = 16 * h; c < nrow; c += 32) {
+                for (int c = 16 * h; c < nrow; c += 16 * H) {
                     uint32_t lo[16], hi[16];
                     tmem_ld16x2(tb + c, tb + 128 + c, lo, hi);
 #pragma unroll
@@ -1035,7 +1042,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 if (old != w.parts - 1) nrow = 0;   // another part comes later: its warp finishes
             }
 #pragma unroll 1
-            for (int c = 16 * h; c < nrow; c += 32) {
+            for (int c = 16 * h; c < nrow; c += 16 * H) {
                 uint32_t lo[16], hi[16];
                 if (w.parts == 1) {
                     tmem_ld16x2(tb + c, tb + 128 + c, lo, hi);
@@ -1046,7 +1053,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         hi[j] = two && c + j < nrow ? static_cast<uint32_t>(__ldcg(sums + (c + j) * 256 + 128)) : 0u;
                     }
                 }
-                const float* sap = my_sa + (c >> 5) * 16;
+                const float* sap = my_sa + c / (16 * H) * 16;
                 float y[SWIGLU ? 16 : 32];
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
@@ -1152,7 +1159,7 @@ bool map_out(CUtensorMap* m, void* base, long long rows, int N, int dtype) {
 }
 
 template <auto KERNEL>
-cudaError_t launch_tc(size_t smem, int grid, const Maps& m, const KP& kp, cudaStream_t st) {
+cudaError_t launch_tc(size_t smem, int grid, int threads, const Maps& m, const KP& kp, cudaStream_t st) {
     static bool attr_set[64] = {};   // per kernel (template) and device; the size never changes
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -1161,7 +1168,7 @@ cudaError_t launch_tc(size_t smem, int grid, const Maps& m, const KP& kp, cudaSt
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    return launch_dep(KERNEL, dim3(grid), dim3(NUM_THREADS), smem, st, m.a, m.b0, m.b1, m.x0, m.x1, kp);
+    return launch_dep(KERNEL, dim3(grid), dim3(threads), smem, st, m.a, m.b0, m.b1, m.x0, m.x1, kp);
 }
 
 template <bool SWIGLU, typename OutT>
@@ -1169,9 +1176,13 @@ cudaError_t launch_form(const I8Gemm& g, const KP& kp, const Maps& m, cudaStream
     if (g.form == I8_PAIR)
         return launch_tc<i8_pair_kernel<SWIGLU, OutT>>(
                          P_STAGES * P_STAGE_BYTES + EPI * (P_STAGE_FLOATS + P_SCALE_FLOATS) * 4 + 1024 + sizeof(Ctl<P_STAGES>),
-                         device_sm_count() & ~1, m, kp, st);
-    return launch_tc<i8_single_kernel<SWIGLU, OutT>>(S_STAGES * S_STAGE_BYTES + EPI * S_ROW_FLOATS * 4 + 1024 + sizeof(Ctl<S_STAGES>),
-                     std::min(device_sm_count(), kI8MaxGrid), m, kp, st);
+                         device_sm_count() & ~1, NUM_THREADS, m, kp, st);
+    const int grid = std::min(device_sm_count(), kI8MaxGrid);
+    constexpr size_t smem = S_STAGES * S_STAGE_BYTES + 1024 + sizeof(Ctl<S_STAGES>);
+    // Few rows: four warps to an accumulator in place of eight, which a launch of one token pays for (49.6 -> 48.8 us and
+    // 30.4 -> 29.7 us, 8 experts, 4096 <-> 14336); 129 rows to each of 68 experts of K = 64 take 49 us with four, 43 with eight.
+    if (g.rows <= 64) return launch_tc<i8_single_kernel<SWIGLU, OutT, 1>>(smem + 8 * S_ROW_FLOATS * 4, grid, 320, m, kp, st);
+    return launch_tc<i8_single_kernel<SWIGLU, OutT, 2>>(smem + 16 * S_ROW_FLOATS * 4, grid, 576, m, kp, st);
 }
 
 }  // namespace
