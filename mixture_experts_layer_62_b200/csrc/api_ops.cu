@@ -29,20 +29,26 @@ I8Layout make_i8_layout(const moe_problem& p) {
     return L;
 }
 
-// CTA pairs need rows to fill their tiles of 256 x 512 (256 of SWIGLU) and
-// tiles to fill the GPU: below 256 rows an expert, or 1.5 tiles a pair of SMs
-// (with half a block an expert for its ragged end), the single form, whose
-// last tiles are cut along K, is faster. Measured, single against pair, top-2
-// of 8 experts (us): up projection 4096 -> 14336 of 1024 rows 197 / 222, of 2048
-// rows 284 / 265, of 8192 rows 904 / 712; down projection 14336 -> 4096 of 2048
-// rows (96 tiles) 134 / 154, of 3000 rows (128 tiles) 185 / 158.
+// CTA pairs need rows to fill their tiles of 256 x 512 (256 of SWIGLU), K
+// blocks to outweigh what a tile costs besides them, channels in 7/10 of their
+// tiles' and tiles for 6/10 of the SM pairs; the single form takes the rest.
+// Measured, single / pair (us), by rows an expert and K:
+//   K = 14336, 4096 channels, 8 experts: 144 rows 133 / 88, 256 rows 135 / 144, 448
+//     rows 208 / 162; K = 4096, 2 x 14336 channels: 128 rows 177 / 199, 192 rows
+//     221 / 212, 1024 rows 877 / 707
+//   K = 2048, 2 x 1408 channels, 64 experts: 352 rows 142 / 154, 448 rows 186 / 167
+//   K = 768, 2048 channels, 128 experts: 352 rows 109 / 120, 640 rows 189 / 178
+//   K = 2048, 640 channels (5/8 of their tiles), 24 experts: 448 rows 26 / 32
+// Over 120 such shapes the choice costs 0.3 % against the better form of each.
 I8Form i8_form(const moe_problem& p, bool down) {
     const long long pairs = (long long)p.T * p.k, E = p.E;
-    if (pairs < 256 * E) return I8_SINGLE;
-    const long long blocks2 = pairs / 128 + E;   // blocks of 256 rows, doubled
-    const long long cols = down ? ceil_div(p.d, 512) : ceil_div(p.d_ff, 256);
+    const int K = down ? p.d_ff : p.d, N = down ? p.d : p.d_ff, wide = down ? 512 : 256;
+    if (pairs < (K >= 4096 ? 128 : K > 1024 ? 400 : 640) * E) return I8_SINGLE;
+    const long long cols = ceil_div(N, wide);
+    if (10ll * N < 7 * cols * wide) return I8_SINGLE;
+    const long long blocks2 = pairs / 128 + E;   // blocks of 256 rows, half a block an expert for its ragged end, doubled
     const int sms = device_sm_count();
-    return 2 * blocks2 * cols >= 3LL * (sms > 0 ? sms : 148) ? I8_PAIR : I8_SINGLE;
+    return 5 * blocks2 * cols >= 3LL * (sms > 0 ? sms : 148) ? I8_PAIR : I8_SINGLE;
 }
 
 }  // namespace moe

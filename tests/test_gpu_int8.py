@@ -392,7 +392,10 @@ def test_variants_by_size():
                                  moe.int8_variant(moe.problem(T, d, dff, E, k), down=True))
     assert v(1, 4096, 14336, 8, 2) == ("single", "single")
     assert v(4096, 4096, 14336, 8, 2) == ("pair", "pair")
-    assert v(1024, 4096, 14336, 8, 2) == ("pair", "single")
+    assert v(1024, 4096, 14336, 8, 2) == ("pair", "pair")
+    assert v(448, 4096, 14336, 8, 2) == ("single", "single")     # 112 rows an expert
+    assert v(1500, 1024, 2048, 8, 2) == ("single", "single")     # 375 rows, short K
+    assert v(4000, 640, 2048, 24, 3) == ("single", "single")     # 500 rows; 640 channels fill 5/8 of their tiles
     assert v(2048, 7168, 2048, 256, 8) == ("single", "single")
 
 
