@@ -17,6 +17,8 @@
 //
 // Sums are fp32 in slot order, each result is rounded once, nothing is
 // atomic: repeated calls give identical bits.
+#include <algorithm>
+
 #include "ops.cuh"
 
 namespace moe {
@@ -99,6 +101,9 @@ __device__ __forceinline__ void drop8(const Dropout& d, unsigned long long seed,
 // vectors of eight columns, the rows of all K slots requested together
 // (K: k rounded up to 1, 2, 4, 8 or 16).
 constexpr int kMixThreads = 128;
+// The threads of a block: a vector of eight columns each, at most kMixThreads. (2876 tokens of d = 152 in fp32, 6 slots,
+// both passes: 9.0 us; with 128 threads always 15.3.)
+inline unsigned mix_threads(int d) { return static_cast<unsigned>(d >= 8 * kMixThreads ? kMixThreads : (d / 8 + 31) / 32 * 32); }
 template <typename T, bool GATED, bool DROP, int K>
 __global__ void __launch_bounds__(kMixThreads)
 mix_kernel(const __grid_constant__ MixArgs a, int slices) {
@@ -122,7 +127,7 @@ mix_kernel(const __grid_constant__ MixArgs a, int slices) {
         offset = a.drop.rng[1];
     }
     const T* o = static_cast<const T*>(a.o);
-    for (int v = v_lo + static_cast<int>(threadIdx.x); v < v_hi; v += kMixThreads) {
+    for (int v = v_lo + static_cast<int>(threadIdx.x); v < v_hi; v += static_cast<int>(blockDim.x)) {
         const size_t col = static_cast<size_t>(v) * 8, at = t * a.d + col;
         Vec8<T> raw[K], rv, sv;
 #pragma unroll
@@ -155,27 +160,29 @@ mix_kernel(const __grid_constant__ MixArgs a, int slices) {
     }
 }
 
-// One block per token: a thread takes every THREADS-th vector of dy, forms
+// One block per token: a thread takes every blockDim-th vector of dy, forms
 // u = D(dy) once and serves all of the token's slots from it; the slots' dot
 // products are summed lane by lane, then over the block in a fixed order.
-// With padding, the first kPadBlocks blocks fill the padding rows of dO with
-// zeros: a warp reads the tokens of 32 rows at once and writes those of none.
-constexpr int kPadBlocks = 148;
-template <typename T, bool DROP, int K, int THREADS>
-__global__ void __launch_bounds__(THREADS)
-mix_back_kernel(const __grid_constant__ MixBackArgs a) {
-    __shared__ float part[THREADS / 32][K];
+// With padding, the first blocks (`pads`) fill the padding rows of dO with
+// zeros: a warp reads the tokens of kPadRows rows at once and writes the rows
+// of none (513 tokens of d = 6208, 52 experts padded to 128 rows, both passes:
+// 44 us; 32 rows a warp took 54).
+constexpr int kPadRows = 8, kMaxPadBlocks = 4 * 148;
+template <typename T, bool DROP, int K, int THREADS>   // THREADS: those of the block, 0: any number up to 512
+__global__ void __launch_bounds__(THREADS > 0 ? THREADS : 512)
+mix_back_kernel(const __grid_constant__ MixBackArgs a, unsigned pads) {
+    __shared__ float part[(THREADS > 0 ? THREADS : 512) / 32][K];
+    const int threads = THREADS > 0 ? THREADS : static_cast<int>(blockDim.x);
     pdl_wait();
     pdl_launch();
     const int nvec = a.d / 8;
     T* dO = static_cast<T*>(a.dO);
-    const unsigned pads = a.row_token != nullptr ? kPadBlocks : 0u;
     if (blockIdx.x < pads) {
         const int used = min(a.indptr[a.E], a.rows), lane = threadIdx.x & 31;
         const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        const int warps = kPadBlocks * (THREADS / 32);
-        for (long long r0 = 32ll * (blockIdx.x + kPadBlocks * (threadIdx.x >> 5)); r0 < used; r0 += 32ll * warps) {
-            const bool none = r0 + lane < used && a.row_token[r0 + lane] < 0;
+        const long long step = static_cast<long long>(kPadRows) * pads * (threads / 32);
+        for (long long r0 = kPadRows * (blockIdx.x + static_cast<long long>(pads) * (threadIdx.x >> 5)); r0 < used; r0 += step) {
+            const bool none = lane < kPadRows && r0 + lane < used && a.row_token[r0 + lane] < 0;
             for (unsigned m = __ballot_sync(0xffffffffu, none); m != 0; m &= m - 1)
                 for (int v = lane; v < nvec; v += 32)
                     Vec8<T>::store(dO + static_cast<size_t>(r0 + __ffs(m) - 1) * a.d + static_cast<size_t>(v) * 8, z);
@@ -197,7 +204,7 @@ mix_back_kernel(const __grid_constant__ MixBackArgs a) {
         seed = a.drop.rng[0];
         offset = a.drop.rng[1];
     }
-    for (int v = threadIdx.x; v < nvec; v += THREADS) {
+    for (int v = threadIdx.x; v < nvec; v += threads) {
         const size_t at = t * a.d + static_cast<size_t>(v) * 8, col = static_cast<size_t>(v) * 8;
         Vec8<T> dyv, ov[K];
         dyv.load(static_cast<const T*>(a.dy) + at);
@@ -231,16 +238,24 @@ mix_back_kernel(const __grid_constant__ MixBackArgs a) {
     __syncthreads();
     if (threadIdx.x < a.k) {
         float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) s += part[w][threadIdx.x];
+        for (int w = 0; w < threads / 32; ++w) s += part[w][threadIdx.x];
         a.dgate[t * a.k + threadIdx.x] = s;
     }
 }
 
 template <typename T, bool DROP, int K>
 cudaError_t mix_back_k(const MixBackArgs& a, cudaStream_t st) {
-    const unsigned grid = static_cast<unsigned>(a.T) + (a.row_token != nullptr ? kPadBlocks : 0);
-    return launch_dep(mix_back_kernel<T, DROP, K, 128>, dim3(grid), dim3(128), 0, st, a);
+    // Less than a block's work for every SM: up to four times the threads to a row (one token of d = 4096, with the
+    // forward pass, 3.9 us in place of 4.2; 64 tokens of d = 7168 and 8 slots 7.8 in place of 8.6; from 200 tokens on it
+    // loses). Blocks of another size than kMixThreads have a kernel of their own, since room for 512 threads leaves each
+    // fewer registers: 8192 tokens of 8 slots take 342 us there and 323 here.
+    unsigned threads = mix_threads(a.d);
+    while (threads < 512 && a.T * threads < 148 * kMixThreads && 8 * threads < static_cast<unsigned>(a.d)) threads *= 2;
+    const unsigned rows = kPadRows * (threads / 32);   // rows of a block's turn
+    const unsigned pads = a.row_token != nullptr ? std::min((static_cast<unsigned>(a.rows) + rows - 1) / rows, kMaxPadBlocks + 0u) : 0u;
+    const dim3 grid(static_cast<unsigned>(a.T) + pads), block(threads);
+    if (threads == kMixThreads) return launch_dep(mix_back_kernel<T, DROP, K, kMixThreads>, grid, block, 0, st, a, pads);
+    return launch_dep(mix_back_kernel<T, DROP, K, 0>, grid, block, 0, st, a, pads);
 }
 template <typename T, bool DROP>
 cudaError_t mix_back_t(const MixBackArgs& a, cudaStream_t st) {
@@ -256,7 +271,7 @@ cudaError_t mix_d(const MixArgs& a, cudaStream_t st) {
     // fewer tokens than two blocks an SM: stretches of the rows, a pass of the threads at least
     int slices = 1;
     while (a.T * slices < 2 * 148 && slices * kMixThreads < a.d / 8) slices *= 2;
-    const dim3 grid(static_cast<unsigned>(a.T) * slices), block(kMixThreads);
+    const dim3 grid(static_cast<unsigned>(a.T) * slices), block(mix_threads(a.d));
     if (a.k <= 1) return launch_dep(mix_kernel<T, GATED, DROP, 1>, grid, block, 0, st, a, slices);
     if (a.k <= 2) return launch_dep(mix_kernel<T, GATED, DROP, 2>, grid, block, 0, st, a, slices);
     if (a.k <= 4) return launch_dep(mix_kernel<T, GATED, DROP, 4>, grid, block, 0, st, a, slices);
