@@ -318,8 +318,10 @@ i8_count_kernel(const int32_t* idx, int T, int k, int kk, int E, int NB, int32_t
 
 // One block: the chunk bases of every expert (prefix over its (slot, chunk)
 // counts), then capacity, padded row offsets and statistics per expert.
-// A warp takes four experts at a time, so that their loads overlap.
+// A warp takes four experts at a time, so that their loads overlap, or one where
+// there are no more than warps.
 constexpr int kScan8Threads = 1024;
+template <int X>   // experts a warp takes at a time
 __global__ void __launch_bounds__(kScan8Threads) i8_scan_kernel(const __grid_constant__ PermuteArgs a, const int32_t* blockcnt,
                                                                 int32_t* blockoff) {
     __shared__ int s_cnt[MOE_MAX_E], s_held[32], s_red[3][32];
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(kScan8Threads) i8_scan_kernel(const __grid_con
     pdl_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int len = a.kk * a.NB;
-    constexpr int X = 4, U = 4;   // experts and steps of 32 entries in flight
+    constexpr int U = 4;   // steps of 32 entries in flight
     for (int e0 = warp * X; e0 < a.E; e0 += 32 * X) {
         int carry[X] = {};
         for (int b0 = 0; b0 < len; b0 += 32 * U) {
@@ -407,10 +409,13 @@ permute_i8_kernel(const __grid_constant__ PermuteArgs a) {
     const int step = gridDim.x * kTokens;
     int t = blockIdx.x * kTokens + sub;
     auto row_of = [&](int tok) { return static_cast<const T*>(a.x) + static_cast<size_t>(tok) * a.d; };
-    pdl_wait();   // !FEW: the chunk bases and indptr come from the scan
-    pdl_launch();
     Vec16<T> A[kHold<T>], B[kHold<T>];
+    if constexpr (FEW) pdl_wait();
     if (t < a.T) hold_row<T, TPR>(A, row_of(t), nv, tid);
+    // The chunk bases and indptr come from the scan. The first rows need not wait for it: the scan lets this kernel start
+    // after the count has ended, which itself has waited for all that came before.
+    if constexpr (!FEW) pdl_wait();
+    pdl_launch();
     const int np = a.T * a.k;
     if constexpr (FEW) {
         for (int i = threadIdx.x; i < np; i += kThreads) s_idx[i] = a.idx[i];
@@ -581,7 +586,7 @@ cudaError_t launch_permute_i8(const PermuteI8& p, cudaStream_t st) {
     cudaError_t e = launch_dep(i8_count_kernel, dim3(a.NB), dim3(kCountThreads), 0, st, p.idx, p.T, p.k, p.kk, p.E, a.NB,
                              p.blockcnt, p.pos);
     if (e != cudaSuccess) return e;
-    e = launch_dep(i8_scan_kernel, dim3(1), dim3(kScan8Threads), 0, st, a, static_cast<const int32_t*>(p.blockcnt), p.blockoff);
+    e = launch_dep(p.E <= 32 ? i8_scan_kernel<1> : i8_scan_kernel<4>, dim3(1), dim3(kScan8Threads), 0, st, a, static_cast<const int32_t*>(p.blockcnt), p.blockoff);
     if (e != cudaSuccess) return e;
     return p.dtype == MOE_DTYPE_BF16 ? permute_t<__nv_bfloat16, false>(a, st) : permute_t<float, false>(a, st);
 }
