@@ -410,6 +410,28 @@ def test_products_in_pairs(T, d, dff, E, k):
         run_products(T, d, dff, E, k, "bf16", ends, gen(cut[0] + 1))
 
 
+@pytest.mark.parametrize("n", [192, 193, 223, 224, 225, 255, 256, 257, 449, 511])
+def test_products_in_pairs_by_last_block(n):
+    # groups whose last block is the largest short one, a whole one with a ragged stretch of 32 rows, a full one
+    T, d, dff, E = 1600, 512, 8192, 2
+    p = moe.problem(T, d, dff, E, 1)
+    assert moe.int8_variant(p) == "pair"
+    run_products(T, d, dff, E, 1, "bf16", torch.tensor([0, n, n + 512 + n % 32], dtype=torch.int32), gen(n))
+
+
+@pytest.mark.parametrize("T,d,dff,E,k", [
+    (40, 256, 8192, 1, 1),       # one or two tiles, K in 16 shares
+    (40, 192, 8192, 3, 1),       # the same, the last 64 channels of 256 alone in their half
+    (65, 320, 4096, 2, 1),       # more than 64 rows
+    (60, 8192, 4096, 4, 1),      # 128 tiles of a 148th each: not cut
+    (260, 1024, 1408, 2, 1),     # tall tiles, short K: not cut
+    (300, 2432, 2560, 2, 1),     # whole tiles and a tail
+])
+def test_products_by_their_tail(T, d, dff, E, k):
+    for s in (0, 1):
+        run_products(T, d, dff, E, k, "bf16", split(T * k, E, s), gen(T + s), ws_fill=255 * s)
+
+
 def test_products_in_pairs_f32():
     T, d, dff, E = 1700, 1040, 4112, 2
     p = moe.problem(T, d, dff, E, 1, 0.0, "f32")
@@ -492,3 +514,40 @@ def test_calls_wait_for_what_comes_before_them():
     for _ in range(3):
         graph.replay()
         check()
+
+
+@pytest.mark.parametrize("T", [500, 3000])
+def test_permutation_waits_for_what_comes_before_it(T):
+    # its rows are read early: behind a slow producer, and right behind a kernel of the library that writes them
+    g = gen(T)
+    d, E, k = 256, 8, 2
+    p = moe.problem(T, d, 64, E, k)
+    src, idx = randn(g, T, d).to(torch.bfloat16), R.routed(T, E, k, T, 0.5).to(torch.int32).to(DEV)
+    rows = moe.permuted_rows(p)
+    x, dead = torch.zeros_like(src), torch.zeros((T, d), dtype=torch.int8, device=DEV)
+    pos, indptr = torch.empty((T, k), dtype=torch.int32, device=DEV), torch.empty(E + 1, dtype=torch.int32, device=DEV)
+    row_token = torch.empty(rows, dtype=torch.int32, device=DEV)
+    xq, xs = torch.zeros((rows, d), dtype=torch.int8, device=DEV), torch.zeros(rows, device=DEV)
+    work, st = moe.alloc_int8_workspace(p, DEV), moe.alloc_stats(E, DEV)
+    # as one expert of one slot and gate 1, the way back copies its rows
+    one = moe.problem(T, d, 64, 1, 1)
+    at, gate = torch.arange(T, dtype=torch.int32, device=DEV).view(T, 1), torch.ones((T, 1), device=DEV)
+
+    def permute():
+        moe.permute_int8(p, x, idx, pos, indptr, row_token, xq, xs, st, work)
+
+    x.copy_(src)
+    permute()
+    torch.cuda.synchronize()
+    want = xq.clone(), xs.clone()
+    for slow in (False, True, True):
+        for t in (x, xq, xs):
+            t.zero_()
+        torch.cuda.synchronize()
+        if slow:
+            torch.cuda._sleep(2_000_000)
+            moe.quantize_rows(src, dead, torch.empty(T, device=DEV))
+        moe.combine_dropout(one, src, at, gate, x)
+        permute()
+        torch.cuda.synchronize()
+        assert torch.equal(x, src) and torch.equal(xq, want[0]) and torch.equal(xs, want[1])

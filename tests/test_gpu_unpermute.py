@@ -15,7 +15,8 @@ CASES = [dict(T=1, d=64, E=4, k=1), dict(T=1, d=4096, E=8, k=2, prob=0.1), dict(
          dict(T=45, d=128, E=7, k=3, cf=0.7, pad=64, shared=True, prob=0.25),
          dict(T=300, d=1024, E=8, k=2, cf=0.5, residual=True, prob=0.9), dict(T=130, d=2112, E=12, k=5, residual=True),
          dict(T=700, d=320, E=64, k=8, cf=1.0, pad=128, shared=True, residual=True, prob=0.05),
-         dict(T=64, d=7168, E=9, k=9, cf=0.6, prob=0.3, shared=True)]
+         dict(T=64, d=7168, E=9, k=9, cf=0.6, prob=0.3, shared=True),
+         dict(T=2500, d=64, E=40, k=3, pad=128, prob=0.1), dict(T=3, d=520 * 8, E=70, k=2, pad=64)]
 
 
 def make(c, dtype, seed=0):
