@@ -131,10 +131,31 @@ def _load():
     lib.moe_combine_backward.restype = ctypes.c_int
     lib.moe_permute_backward.argtypes = [P] + [vp] * 4
     lib.moe_permute_backward.restype = ctypes.c_int
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise ImportError("the package's binding is missing for this Python: build it with "
+                          "`python -m mixture_experts_layer_62_b200.build`") from e
+    _binding.attach(tuple(ctypes.cast(getattr(lib, "moe_" + n), vp).value for n in _BOUND))
+    global _BINDING
+    _BINDING = _binding
     return lib
 
 
+# calls that csrc/binding.cpp makes, in its order
+_BOUND = ("quantize_rows", "permute_int8", "expert_up_int8", "expert_down_int8", "combine_dropout", "combine_backward",
+          "permute_backward")
+_BINDING = None
 _LIB = None
+
+
+def _bound():
+    """The binding: its functions return a call's code, or None, with nothing
+    done, where an argument is not as it has to be (the checks in this file
+    then say which)."""
+    if _BINDING is None:
+        _lib()
+    return _BINDING
 
 
 def _lib():
@@ -436,16 +457,18 @@ def quantize_rows(x, q=None, scale=None, used=None, stream=None):
     """Rows of x [..., cols] in 8 bits with a scale for each row (see
     moe_quantize_rows); used: a one-element int32 tensor, the rows to take.
     Returns (q, scale), allocated here when not given."""
-    dev = _device(x)
-    dt, n, cols = x.dtype, x.numel(), x.shape[-1]
-    rows = n // cols if cols else 0
     if q is None:
         q = torch.empty(x.shape, dtype=_I8, device=x.device)
     if scale is None:
         scale = torch.empty(x.shape[:-1], dtype=_F32, device=x.device)
-    rc = _lib().moe_quantize_rows(_dtype_code(dt), _arg(x, dt, n, "x", dev), rows, cols,
-                                  _opt(used, _I32, 1, "used", dev), _arg(q, _I8, n, "q", dev),
-                                  _arg(scale, _F32, rows, "scale", dev), _on(stream, dev))
+    rc = _bound().quantize_rows(x, q, scale, used, stream)
+    if rc is None:
+        dev = _device(x)
+        dt, n, cols = x.dtype, x.numel(), x.shape[-1]
+        rows = n // cols if cols else 0
+        rc = _lib().moe_quantize_rows(_dtype_code(dt), _arg(x, dt, n, "x", dev), rows, cols,
+                                      _opt(used, _I32, 1, "used", dev), _arg(q, _I8, n, "q", dev),
+                                      _arg(scale, _F32, rows, "scale", dev), _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_quantize_rows")
     return q, scale
@@ -453,42 +476,48 @@ def quantize_rows(x, q=None, scale=None, used=None, stream=None):
 
 def permute_int8(p: Problem, x, idx, pos, indptr, row_token, xq, xs, stats, workspace, stream=None):
     """moe_permute with the token rows in 8 bits (see moe_permute_int8)."""
-    dev, T, d, E = _device(x), p.T, p.d, p.E
-    rows, pairs = _rows(p), T * p.k
-    rc = _lib().moe_permute_int8(
-        ctypes.byref(p), _arg(x, torch_dtype(p.dtype), T * d, "x", dev), _arg(idx, _I32, pairs, "idx", dev),
-        _arg(pos, _I32, pairs, "pos", dev), _arg(indptr, _I32, E + 1, "indptr", dev),
-        _arg(row_token, _I32, rows, "row_token", dev), _arg(xq, _I8, rows * d, "xq", dev),
-        _arg(xs, _F32, rows, "xs", dev), _arg(stats, _U8, STATS_HEADER_BYTES + 16 * E, "stats", dev),
-        _arg(workspace, _U8, 0, "workspace", dev), workspace.nbytes, _on(stream, dev))
+    rc = _bound().permute_int8(p, x, idx, pos, indptr, row_token, xq, xs, stats, workspace, stream)
+    if rc is None:
+        dev, T, d, E = _device(x), p.T, p.d, p.E
+        rows, pairs = _rows(p), T * p.k
+        rc = _lib().moe_permute_int8(
+            ctypes.byref(p), _arg(x, torch_dtype(p.dtype), T * d, "x", dev), _arg(idx, _I32, pairs, "idx", dev),
+            _arg(pos, _I32, pairs, "pos", dev), _arg(indptr, _I32, E + 1, "indptr", dev),
+            _arg(row_token, _I32, rows, "row_token", dev), _arg(xq, _I8, rows * d, "xq", dev),
+            _arg(xs, _F32, rows, "xs", dev), _arg(stats, _U8, STATS_HEADER_BYTES + 16 * E, "stats", dev),
+            _arg(workspace, _U8, 0, "workspace", dev), workspace.nbytes, _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_permute_int8")
 
 
 def expert_up_int8(p: Problem, xq, xs, indptr, W1, w1s, W3, w3s, h, workspace, stats=None, stream=None):
     """h = SiLU(a) b over 8-bit rows and weights with their scales; see moe_expert_up_int8."""
-    dev, rows, E, d, dff = _device(xq), _rows(p), p.E, p.d, p.d_ff
-    n = E * dff
-    rc = _lib().moe_expert_up_int8(
-        ctypes.byref(p), _arg(xq, _I8, rows * d, "xq", dev), _arg(xs, _F32, rows, "xs", dev),
-        _arg(indptr, _I32, E + 1, "indptr", dev), _arg(W1, _I8, n * d, "W1", dev), _arg(w1s, _F32, n, "w1s", dev),
-        _arg(W3, _I8, n * d, "W3", dev), _arg(w3s, _F32, n, "w3s", dev),
-        _arg(h, torch_dtype(p.dtype), rows * dff, "h", dev),
-        _opt(stats, _U8, STATS_HEADER_BYTES, "stats", dev), _arg(workspace, _U8, 0, "workspace", dev),
-        workspace.nbytes, _on(stream, dev))
+    rc = _bound().expert_up_int8(p, xq, xs, indptr, W1, w1s, W3, w3s, h, stats, workspace, stream)
+    if rc is None:
+        dev, rows, E, d, dff = _device(xq), _rows(p), p.E, p.d, p.d_ff
+        n = E * dff
+        rc = _lib().moe_expert_up_int8(
+            ctypes.byref(p), _arg(xq, _I8, rows * d, "xq", dev), _arg(xs, _F32, rows, "xs", dev),
+            _arg(indptr, _I32, E + 1, "indptr", dev), _arg(W1, _I8, n * d, "W1", dev), _arg(w1s, _F32, n, "w1s", dev),
+            _arg(W3, _I8, n * d, "W3", dev), _arg(w3s, _F32, n, "w3s", dev),
+            _arg(h, torch_dtype(p.dtype), rows * dff, "h", dev),
+            _opt(stats, _U8, STATS_HEADER_BYTES, "stats", dev), _arg(workspace, _U8, 0, "workspace", dev),
+            workspace.nbytes, _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_expert_up_int8")
 
 
 def expert_down_int8(p: Problem, hq, hs, indptr, W2, w2s, o, workspace, stats=None, stream=None):
     """o = hq W2^T over 8-bit rows and weights with their scales; see moe_expert_down_int8."""
-    dev, rows, E, d, dff = _device(hq), _rows(p), p.E, p.d, p.d_ff
-    n = E * d
-    rc = _lib().moe_expert_down_int8(
-        ctypes.byref(p), _arg(hq, _I8, rows * dff, "hq", dev), _arg(hs, _F32, rows, "hs", dev),
-        _arg(indptr, _I32, E + 1, "indptr", dev), _arg(W2, _I8, n * dff, "W2", dev), _arg(w2s, _F32, n, "w2s", dev),
-        _arg(o, torch_dtype(p.dtype), rows * d, "o", dev), _opt(stats, _U8, STATS_HEADER_BYTES, "stats", dev),
-        _arg(workspace, _U8, 0, "workspace", dev), workspace.nbytes, _on(stream, dev))
+    rc = _bound().expert_down_int8(p, hq, hs, indptr, W2, w2s, o, stats, workspace, stream)
+    if rc is None:
+        dev, rows, E, d, dff = _device(hq), _rows(p), p.E, p.d, p.d_ff
+        n = E * d
+        rc = _lib().moe_expert_down_int8(
+            ctypes.byref(p), _arg(hq, _I8, rows * dff, "hq", dev), _arg(hs, _F32, rows, "hs", dev),
+            _arg(indptr, _I32, E + 1, "indptr", dev), _arg(W2, _I8, n * dff, "W2", dev), _arg(w2s, _F32, n, "w2s", dev),
+            _arg(o, torch_dtype(p.dtype), rows * d, "o", dev), _opt(stats, _U8, STATS_HEADER_BYTES, "stats", dev),
+            _arg(workspace, _U8, 0, "workspace", dev), workspace.nbytes, _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_expert_down_int8")
 
@@ -505,11 +534,13 @@ def _rng(rng, dev):
 def combine_dropout(p: Problem, o, pos, gate, out, s=None, residual=None, prob=0.0, rng=None, stream=None):
     """out_t = residual_t + dropout(sum_j gate[t,j] o[pos[t,j]] (+ s_t)); rng: a
     device tensor of two 64-bit integers (seed, offset). See moe_combine_dropout."""
-    dev, dt, n, pairs = _device(o), torch_dtype(p.dtype), p.T * p.d, p.T * p.k
-    rc = _lib().moe_combine_dropout(
-        ctypes.byref(p), _arg(o, dt, _rows(p) * p.d, "o", dev), _arg(pos, _I32, pairs, "pos", dev),
-        _arg(gate, _F32, pairs, "gate", dev), _opt(s, dt, n, "s", dev), _opt(residual, dt, n, "residual", dev), prob,
-        _rng(rng, dev), _arg(out, dt, n, "out", dev), _on(stream, dev))
+    rc = _bound().combine_dropout(p, o, pos, gate, s, residual, prob, rng, out, stream)
+    if rc is None:
+        dev, dt, n, pairs = _device(o), torch_dtype(p.dtype), p.T * p.d, p.T * p.k
+        rc = _lib().moe_combine_dropout(
+            ctypes.byref(p), _arg(o, dt, _rows(p) * p.d, "o", dev), _arg(pos, _I32, pairs, "pos", dev),
+            _arg(gate, _F32, pairs, "gate", dev), _opt(s, dt, n, "s", dev), _opt(residual, dt, n, "residual", dev), prob,
+            _rng(rng, dev), _arg(out, dt, n, "out", dev), _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_combine_dropout")
     return out
@@ -520,25 +551,29 @@ def combine_backward(p: Problem, dy, o, pos, gate, dO, dgate, ds=None, prob=0.0,
     """Gradients of combine_dropout with the same prob and rng values:
     dO[pos] = gate u, dgate = <u, o[pos]>, ds = u with u = dropout(dy); indptr
     and row_token are needed with p.pad_rows > 0. See moe_combine_backward."""
-    dev, dt, n, pairs, rows = _device(dy), torch_dtype(p.dtype), p.T * p.d, p.T * p.k, _rows(p)
-    ends = tokens = None
-    if p.pad_rows > 0:
-        ends, tokens = _opt(indptr, _I32, p.E + 1, "indptr", dev), _opt(row_token, _I32, rows, "row_token", dev)
-    rc = _lib().moe_combine_backward(
-        ctypes.byref(p), _arg(dy, dt, n, "dy", dev), _arg(o, dt, rows * p.d, "o", dev),
-        _arg(pos, _I32, pairs, "pos", dev), _arg(gate, _F32, pairs, "gate", dev), prob, _rng(rng, dev), ends, tokens,
-        _arg(dO, dt, rows * p.d, "dO", dev), _arg(dgate, _F32, pairs, "dgate", dev), _opt(ds, dt, n, "ds", dev),
-        _on(stream, dev))
+    rc = _bound().combine_backward(p, dy, o, pos, gate, prob, rng, indptr, row_token, dO, dgate, ds, stream)
+    if rc is None:
+        dev, dt, n, pairs, rows = _device(dy), torch_dtype(p.dtype), p.T * p.d, p.T * p.k, _rows(p)
+        ends = tokens = None
+        if p.pad_rows > 0:
+            ends, tokens = _opt(indptr, _I32, p.E + 1, "indptr", dev), _opt(row_token, _I32, rows, "row_token", dev)
+        rc = _lib().moe_combine_backward(
+            ctypes.byref(p), _arg(dy, dt, n, "dy", dev), _arg(o, dt, rows * p.d, "o", dev),
+            _arg(pos, _I32, pairs, "pos", dev), _arg(gate, _F32, pairs, "gate", dev), prob, _rng(rng, dev), ends, tokens,
+            _arg(dO, dt, rows * p.d, "dO", dev), _arg(dgate, _F32, pairs, "dgate", dev), _opt(ds, dt, n, "ds", dev),
+            _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_combine_backward")
 
 
 def permute_backward(p: Problem, dxp, pos, dx, stream=None):
     """dx_t = sum_j dxp[pos[t,j]] over the kept pairs; see moe_permute_backward."""
-    dev, dt = _device(dxp), torch_dtype(p.dtype)
-    rc = _lib().moe_permute_backward(ctypes.byref(p), _arg(dxp, dt, _rows(p) * p.d, "dxp", dev),
-                                     _arg(pos, _I32, p.T * p.k, "pos", dev), _arg(dx, dt, p.T * p.d, "dx", dev),
-                                     _on(stream, dev))
+    rc = _bound().permute_backward(p, dxp, pos, dx, stream)
+    if rc is None:
+        dev, dt = _device(dxp), torch_dtype(p.dtype)
+        rc = _lib().moe_permute_backward(ctypes.byref(p), _arg(dxp, dt, _rows(p) * p.d, "dxp", dev),
+                                         _arg(pos, _I32, p.T * p.k, "pos", dev), _arg(dx, dt, p.T * p.d, "dx", dev),
+                                         _on(stream, dev))
     if rc:
         raise MoEError(rc, "moe_permute_backward")
     return dx

@@ -9,6 +9,9 @@ point for tensor maps is looked up at run time, so no libcuda link is needed.
 With --debug (or build(debug=True)) the same sources are compiled with
 MOE_DEBUG into _build_debug/ and libmoe_debug.so: the library with the
 device-side bounds checks that record MOE_ERR_BOUNDS (include/moe.h).
+Either way csrc/binding.cpp, the package's own calls of some of the library's
+functions, is compiled for the running Python and torch with the host's C++
+compiler.
 """
 
 from __future__ import annotations
@@ -18,6 +21,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -28,6 +32,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libmoe.so")
 DEBUG_BUILD_DIR = os.path.join(ROOT, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libmoe_debug.so")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 SOURCES = ["api.cu", "route.cu", "permute.cu", "combine.cu", "gemm_simt.cu", "gemm_sm100.cu",
            "permute_noalloc.cu", "route_small.cu", "gemm_bwd_sm100.cu", "bwd.cu",
@@ -80,7 +85,7 @@ def build(force=False, verbose=False, extra_flags=(), debug=False):
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"the compiler failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr, flush=True)
 
@@ -89,6 +94,15 @@ def build(force=False, verbose=False, extra_flags=(), debug=False):
     if force or jobs or _stale(lib_path, objs):
         cmd = [nvcc, *ARCH_FLAGS, "-shared", "-o", lib_path, *objs]
         run(cmd)
+    src = os.path.join(CSRC, "binding.cpp")
+    if force or _stale(BINDING_PATH, [src, os.path.join(INCLUDE, "moe.h")]):
+        import torch
+        home = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+        incs = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(home, "include"), os.path.join(cuda, "include")]
+        run([os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+             *[f for i in incs for f in ("-I", i)], src, "-o", BINDING_PATH, "-L", os.path.join(home, "lib"),
+             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
     return lib_path
 
 

@@ -1,0 +1,291 @@
+// The calls of api_ops.cu from Python without the cost of ctypes and of checks
+// in Python, which took as long as the launches themselves. Each function looks
+// at every tensor once (type, elements, device, contiguity, address) and makes
+// the library's call. It returns the call's code, or None, with nothing done,
+// when an argument is not as it has to be: the caller then goes through its
+// own checks, which say what is wrong. Microseconds of the host for a pass of 9
+// tokens, d = d_ff = 64, against ctypes: quantisation and down product 16.0 ->
+// 9.1, permutation and up product 18.4 -> 9.6, the way back and its gradient
+// 13.2 -> 5.4.
+#define PY_SSIZE_T_CLEAN
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+
+#include "moe.h"
+
+namespace {
+
+using at::ScalarType;
+
+enum { QUANTIZE, PERMUTE, UP, DOWN, COMBINE, COMBINE_BACK, PERMUTE_BACK, CALLS };
+constexpr ScalarType I8 = at::kChar, I32 = at::kInt, F32 = at::kFloat, U8 = at::kByte, BF16 = at::kBFloat16;
+void* g_call[CALLS];
+PyObject* s_cuda_stream;
+
+struct Args {
+    bool ok;        // every argument so far is as it has to be
+    int dev;        // current device
+    void* stream;
+    moe_problem p;
+    long long rows, pairs;
+    ScalarType dt;  // the problem's element type
+};
+
+// Address of a tensor of type dt with at least n elements, contiguous, on the current device.
+template <typename T = void>
+T* tensor(Args* a, PyObject* o, ScalarType dt, long long n) {
+    if (!a->ok) return nullptr;
+    a->ok = false;
+    if (!THPVariable_Check(o)) return nullptr;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.scalar_type() != dt || t.numel() < n || !t.is_cuda() || t.get_device() != a->dev || !t.is_contiguous()) return nullptr;
+    a->ok = true;
+    return static_cast<T*>(t.data_ptr());
+}
+template <typename T = void>
+T* optional(Args* a, PyObject* o, ScalarType dt, long long n) {
+    return o == Py_None ? nullptr : tensor<T>(a, o, dt, n);
+}
+const uint64_t* generator(Args* a, PyObject* o) {
+    if (o == Py_None || !a->ok) return nullptr;
+    const bool u = THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kUInt64;
+    return tensor<const uint64_t>(a, o, u ? at::kUInt64 : at::kLong, 2);
+}
+size_t bytes_of(const Args& a, PyObject* o) {   // of a uint8 tensor
+    return a.ok ? static_cast<size_t>(THPVariable_Unpack(o).numel()) : 0;
+}
+
+// The current device and the stream: the device's current one, a stream object or a handle.
+void begin(Args* a, PyObject* stream) {
+    a->ok = false;
+    a->dev = c10::cuda::current_device();
+    if (stream == Py_None) {
+        a->stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(a->dev)).stream();
+    } else {
+        PyObject* s = PyLong_Check(stream) ? Py_NewRef(stream) : PyObject_GetAttr(stream, s_cuda_stream);
+        if (s == nullptr) return;
+        a->stream = PyLong_AsVoidPtr(s);
+        Py_DECREF(s);
+    }
+    a->ok = PyErr_Occurred() == nullptr;
+}
+void problem(Args* a, PyObject* p, PyObject* stream) {
+    begin(a, stream);
+    if (!a->ok) return;
+    a->ok = false;
+    Py_buffer v;
+    if (PyObject_GetBuffer(p, &v, PyBUF_SIMPLE) != 0) return;
+    if (v.len == (Py_ssize_t)sizeof(moe_problem)) {
+        a->p = *(const moe_problem*)v.buf;
+        a->pairs = (long long)a->p.T * a->p.k;
+        a->rows = a->pairs + (a->p.pad_rows > 0 ? (long long)a->p.E * (a->p.pad_rows - 1) : 0);
+        a->dt = a->p.dtype == MOE_DTYPE_BF16 ? BF16 : F32;
+        // sizes whose products stay within 64 bits; others are the caller's to refuse
+        const int max = 1 << 22;
+        a->ok = (a->p.dtype == MOE_DTYPE_BF16 || a->p.dtype == MOE_DTYPE_F32) && a->p.T >= 0 && a->p.d >= 0 && a->p.d <= max &&
+                a->p.d_ff >= 0 && a->p.d_ff <= max && a->p.E >= 0 && a->p.E <= MOE_MAX_E && a->p.k >= 0 && a->p.k <= MOE_MAX_K;
+    }
+    PyBuffer_Release(&v);
+}
+PyObject* answer(bool ok, int rc) {
+    PyErr_Clear();
+    if (!ok) Py_RETURN_NONE;
+    return PyLong_FromLong(rc);
+}
+#define CALL(id, type, ...)                    \
+    int rc = 0;                                \
+    if (a.ok) {                                \
+        Py_BEGIN_ALLOW_THREADS                 \
+        rc = ((type)g_call[id])(__VA_ARGS__);  \
+        Py_END_ALLOW_THREADS                   \
+    }                                          \
+    return answer(a.ok, rc)
+#define ARGS(count)                                                            \
+    if (n != (count)) {                                                        \
+        PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", (count), n); \
+        return NULL;                                                           \
+    }                                                                          \
+    Args a
+
+// x, q, scale, used, stream
+PyObject* quantize_rows(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+    ARGS(5);
+    begin(&a, v[4]);
+    long long cols = 0, all = 0;
+    ScalarType dt = F32;
+    if (a.ok && (a.ok = THPVariable_Check(v[0]))) {
+        const at::Tensor& t = THPVariable_Unpack(v[0]);
+        dt = t.scalar_type();
+        all = t.numel();
+        cols = t.dim() > 0 ? t.size(t.dim() - 1) : 0;
+        a.ok = cols > 0 && all / cols <= INT32_MAX && cols <= INT32_MAX && (dt == BF16 || dt == F32);
+    }
+    const long long rows = a.ok ? all / cols : 0;
+    const void* x = tensor<const void>(&a, v[0], dt, all);
+    const int32_t* used = optional<const int32_t>(&a, v[3], I32, 1);
+    int8_t* q = tensor<int8_t>(&a, v[1], I8, all);
+    float* scale = tensor<float>(&a, v[2], F32, rows);
+    CALL(QUANTIZE, int (*)(int32_t, const void*, int32_t, int32_t, const int32_t*, int8_t*, float*, void*),
+         dt == BF16 ? MOE_DTYPE_BF16 : MOE_DTYPE_F32, x, (int32_t)rows, (int32_t)cols, used, q, scale, a.stream);
+}
+
+// p, x, idx, pos, indptr, row_token, xq, xs, stats, workspace, stream
+PyObject* permute_int8(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+    ARGS(11);
+    problem(&a, v[0], v[10]);
+    if (!a.ok) return answer(false, 0);
+    const long long d = a.p.d, E = a.p.E;
+    const void* x = tensor<const void>(&a, v[1], a.dt, a.p.T * d);
+    const int32_t* idx = tensor<const int32_t>(&a, v[2], I32, a.pairs);
+    int32_t* pos = tensor<int32_t>(&a, v[3], I32, a.pairs);
+    int32_t* indptr = tensor<int32_t>(&a, v[4], I32, E + 1);
+    int32_t* row_token = tensor<int32_t>(&a, v[5], I32, a.rows);
+    int8_t* xq = tensor<int8_t>(&a, v[6], I8, a.rows * d);
+    float* xs = tensor<float>(&a, v[7], F32, a.rows);
+    void* stats = tensor<void>(&a, v[8], U8, (long long)sizeof(moe_stats) + 16 * E);
+    void* ws = tensor<void>(&a, v[9], U8, 0);
+    const size_t bytes = bytes_of(a, v[9]);
+    CALL(PERMUTE, int (*)(const moe_problem*, const void*, const int32_t*, int32_t*, int32_t*, int32_t*, int8_t*, float*,
+                          void*, void*, size_t, void*),
+         &a.p, x, idx, pos, indptr, row_token, xq, xs, stats, ws, bytes, a.stream);
+}
+
+// p, xq, xs, indptr, W1, w1s, W3, w3s, h, stats, workspace, stream
+PyObject* expert_up_int8(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+    ARGS(12);
+    problem(&a, v[0], v[11]);
+    if (!a.ok) return answer(false, 0);
+    const long long d = a.p.d, f = a.p.d_ff, m = a.p.E * f;
+    const int8_t* xq = tensor<const int8_t>(&a, v[1], I8, a.rows * d);
+    const float* xs = tensor<const float>(&a, v[2], F32, a.rows);
+    const int32_t* indptr = tensor<const int32_t>(&a, v[3], I32, (long long)a.p.E + 1);
+    const int8_t* W1 = tensor<const int8_t>(&a, v[4], I8, m * d);
+    const float* w1s = tensor<const float>(&a, v[5], F32, m);
+    const int8_t* W3 = tensor<const int8_t>(&a, v[6], I8, m * d);
+    const float* w3s = tensor<const float>(&a, v[7], F32, m);
+    void* h = tensor<void>(&a, v[8], a.dt, a.rows * f);
+    void* stats = optional<void>(&a, v[9], U8, (long long)sizeof(moe_stats));
+    void* ws = tensor<void>(&a, v[10], U8, 0);
+    const size_t bytes = bytes_of(a, v[10]);
+    CALL(UP, int (*)(const moe_problem*, const int8_t*, const float*, const int32_t*, const int8_t*, const float*,
+                     const int8_t*, const float*, void*, void*, void*, size_t, void*),
+         &a.p, xq, xs, indptr, W1, w1s, W3, w3s, h, stats, ws, bytes, a.stream);
+}
+
+// p, hq, hs, indptr, W2, w2s, o, stats, workspace, stream
+PyObject* expert_down_int8(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+    ARGS(10);
+    problem(&a, v[0], v[9]);
+    if (!a.ok) return answer(false, 0);
+    const long long d = a.p.d, f = a.p.d_ff, m = a.p.E * d;
+    const int8_t* hq = tensor<const int8_t>(&a, v[1], I8, a.rows * f);
+    const float* hs = tensor<const float>(&a, v[2], F32, a.rows);
+    const int32_t* indptr = tensor<const int32_t>(&a, v[3], I32, (long long)a.p.E + 1);
+    const int8_t* W2 = tensor<const int8_t>(&a, v[4], I8, m * f);
+    const float* w2s = tensor<const float>(&a, v[5], F32, m);
+    void* o = tensor<void>(&a, v[6], a.dt, a.rows * d);
+    void* stats = optional<void>(&a, v[7], U8, (long long)sizeof(moe_stats));
+    void* ws = tensor<void>(&a, v[8], U8, 0);
+    const size_t bytes = bytes_of(a, v[8]);
+    CALL(DOWN, int (*)(const moe_problem*, const int8_t*, const float*, const int32_t*, const int8_t*, const float*, void*,
+                       void*, void*, size_t, void*),
+         &a.p, hq, hs, indptr, W2, w2s, o, stats, ws, bytes, a.stream);
+}
+
+float number(Args* a, PyObject* v) {
+    const double x = PyFloat_AsDouble(v);
+    if (x == -1.0 && PyErr_Occurred()) a->ok = 0;
+    return (float)x;
+}
+
+// p, o, pos, gate, s, residual, prob, rng, out, stream
+PyObject* combine_dropout(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+    ARGS(10);
+    problem(&a, v[0], v[9]);
+    if (!a.ok) return answer(false, 0);
+    const long long d = a.p.d, m = a.p.T * d;
+    const void* o = tensor<const void>(&a, v[1], a.dt, a.rows * d);
+    const int32_t* pos = tensor<const int32_t>(&a, v[2], I32, a.pairs);
+    const float* gate = tensor<const float>(&a, v[3], F32, a.pairs);
+    const void* s = optional<const void>(&a, v[4], a.dt, m);
+    const void* residual = optional<const void>(&a, v[5], a.dt, m);
+    const float prob = number(&a, v[6]);
+    const uint64_t* rng = generator(&a, v[7]);
+    void* out = tensor<void>(&a, v[8], a.dt, m);
+    CALL(COMBINE, int (*)(const moe_problem*, const void*, const int32_t*, const float*, const void*, const void*, float,
+                          const uint64_t*, void*, void*),
+         &a.p, o, pos, gate, s, residual, prob, rng, out, a.stream);
+}
+
+// p, dy, o, pos, gate, prob, rng, indptr, row_token, dO, dgate, ds, stream
+PyObject* combine_backward(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+    ARGS(13);
+    problem(&a, v[0], v[12]);
+    if (!a.ok) return answer(false, 0);
+    const long long d = a.p.d, m = a.p.T * d;
+    const int padded = a.p.pad_rows > 0;
+    const void* dy = tensor<const void>(&a, v[1], a.dt, m);
+    const void* o = tensor<const void>(&a, v[2], a.dt, a.rows * d);
+    const int32_t* pos = tensor<const int32_t>(&a, v[3], I32, a.pairs);
+    const float* gate = tensor<const float>(&a, v[4], F32, a.pairs);
+    const float prob = number(&a, v[5]);
+    const uint64_t* rng = generator(&a, v[6]);
+    const int32_t* indptr = padded ? optional<const int32_t>(&a, v[7], I32, (long long)a.p.E + 1) : nullptr;
+    const int32_t* row_token = padded ? optional<const int32_t>(&a, v[8], I32, a.rows) : nullptr;
+    void* dO = tensor<void>(&a, v[9], a.dt, a.rows * d);
+    float* dgate = tensor<float>(&a, v[10], F32, a.pairs);
+    void* ds = optional<void>(&a, v[11], a.dt, m);
+    CALL(COMBINE_BACK, int (*)(const moe_problem*, const void*, const void*, const int32_t*, const float*, float,
+                               const uint64_t*, const int32_t*, const int32_t*, void*, float*, void*, void*),
+         &a.p, dy, o, pos, gate, prob, rng, indptr, row_token, dO, dgate, ds, a.stream);
+}
+
+// p, dxp, pos, dx, stream
+PyObject* permute_backward(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+    ARGS(5);
+    problem(&a, v[0], v[4]);
+    if (!a.ok) return answer(false, 0);
+    const long long d = a.p.d;
+    const void* dxp = tensor<const void>(&a, v[1], a.dt, a.rows * d);
+    const int32_t* pos = tensor<const int32_t>(&a, v[2], I32, a.pairs);
+    void* dx = tensor<void>(&a, v[3], a.dt, a.p.T * d);
+    CALL(PERMUTE_BACK, int (*)(const moe_problem*, const void*, const int32_t*, void*, void*), &a.p, dxp, pos, dx, a.stream);
+}
+
+// addresses of the library's functions
+PyObject* attach(PyObject* self, PyObject* calls) {
+    if (!PyTuple_Check(calls) || PyTuple_GET_SIZE(calls) != CALLS) {
+        PyErr_SetString(PyExc_ValueError, "attach: the library's functions, in order");
+        return nullptr;
+    }
+    for (int i = 0; i < CALLS; ++i) {
+        g_call[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(calls, i));
+        if (PyErr_Occurred()) return nullptr;
+    }
+    Py_RETURN_NONE;
+}
+
+// what throws here (a tensor without memory, no device) is the caller's to report too
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+    try {
+        return F(self, v, n);
+    } catch (...) {
+        return answer(false, 0);
+    }
+}
+#define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<name>)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {{"attach", attach, METH_O, nullptr},
+                         FAST(quantize_rows), FAST(permute_int8), FAST(expert_up_int8), FAST(expert_down_int8),
+                         FAST(combine_dropout), FAST(combine_backward), FAST(permute_backward),
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__binding(void) {
+    s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
+    return PyModule_Create(&module);
+}
