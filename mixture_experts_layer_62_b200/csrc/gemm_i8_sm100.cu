@@ -18,7 +18,7 @@
 //    rows (cta_group::2), each CTA loading half of both; groups of many rows.
 //    Bound by the tensor pipe and the board's power: 8192 rows, K = 14336,
 //    18944 channels run at 3.3 P operations/s, twice the measured bf16 GEMM
-//    rate; with K = 4096 (Mixtral-shaped up projection, 8 experts, 700 us, 2.75
+//    rate; with K = 4096 (Mixtral-shaped up projection, 8 experts, 690 us, 2.8
 //    P/s) the SwiGLU epilogue and the ragged blocks show. What the tile's
 //    width buys: with 256 x 256 tiles the L2 has to deliver a third more bytes
 //    for the same products, and K = 14336 took 1449 us instead of 1365.
