@@ -551,3 +551,28 @@ def test_permutation_waits_for_what_comes_before_it(T):
         permute()
         torch.cuda.synchronize()
         assert torch.equal(x, src) and torch.equal(xq, want[0]) and torch.equal(xs, want[1])
+
+
+def test_binding_takes_what_is_right_and_nothing_else():
+    b, g = moe._bound(), gen(4)
+    x = randn(g, 8, 64).to(torch.bfloat16)
+    q, s = torch.zeros((8, 64), dtype=torch.int8, device=DEV), torch.zeros(8, device=DEV)
+    want = moe.quantize_rows(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side, side.cuda_stream, 0):
+        q.zero_(), s.zero_()
+        torch.cuda.synchronize()
+        assert b.quantize_rows(x, q, s, None, stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(q, want[0]) and torch.equal(s, want[1])
+    q.zero_()
+    for bad in ((x.cpu(), q, s), (x, q.cpu(), s), (x, q[:7], s), (x, q, s[:7]), (x, q, s.double()), (x.t(), q, s),
+                (x, q.t(), s), (x, q.view(torch.uint8), s), (x.half(), q, s)):
+        assert b.quantize_rows(*bad, None, None) is None
+    assert b.quantize_rows(x, q, s, torch.zeros(1, device=DEV), None) is None
+    # the library's own refusals come through as its codes
+    assert b.quantize_rows(x.view(-1)[:504].view(8, 63), q, s, None, None) == moe.MOE_ERR_UNSUPPORTED
+    assert b.quantize_rows(x.view(-1)[4:68].view(1, 64), q, s, None, None) == moe.MOE_ERR_INVALID_ARG   # 8 bytes off
+    torch.cuda.synchronize()
+    assert not q.any()

@@ -146,3 +146,27 @@ def test_binding_refuses_what_it_can_see(monkeypatch):
     with pytest.raises(ValueError, match="rng"):
         moe.combine_dropout(p, FakeCuda(bf, 256), FakeCuda(i32, 4), FakeCuda(f32, 4), FakeCuda(bf, 256), prob=0.5,
                             rng=FakeCuda(f32, 2))
+
+
+def test_binding_leaves_what_it_does_not_take():
+    # None: nothing was called, the checks in Python say what is wrong
+    b = moe._bound()
+    p = moe.problem(4, 64, 64, 2, 1)
+    host = torch.zeros((4, 64), dtype=torch.bfloat16)
+    ghost = torch.empty((4, 64), dtype=torch.bfloat16, device="meta")
+    q, s = torch.zeros((4, 64), dtype=torch.int8), torch.zeros(4)
+    for x in (host, ghost, None, 3, "x", host.to(torch.float16), host[:, :0], torch.zeros(())):
+        assert b.quantize_rows(x, q, s, None, None) is None
+        assert b.permute_backward(p, x, s, x, None) is None
+    for wrong in (None, 5, b"short", object()):
+        assert b.permute_backward(wrong, host, s, host, None) is None
+        assert b.expert_down_int8(wrong, q, s, s, q, s, host, None, s, None) is None
+    assert b.combine_dropout(p, host, s, s, None, None, "a number", None, host, object()) is None
+    with pytest.raises(TypeError):
+        b.permute_backward(p)
+    with pytest.raises(ValueError):
+        b.attach((1, 2))
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.quantize_rows(host, q, s)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.permute_backward(p, host, s, host)
