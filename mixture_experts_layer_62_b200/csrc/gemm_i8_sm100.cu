@@ -399,6 +399,7 @@ __device__ __forceinline__ void whole_tile(const KP& p, const Item& it, uint32_t
 #pragma unroll 1
     for (int c = 0; c < HALF; c += 16) {
         uint32_t a[16], b[SWIGLU ? 16 : 1];
+        __syncwarp();   // the loads are the warp's: all lanes come to them together
         if constexpr (SWIGLU) tmem_ld16x2(tb + HALF * h + c, tb + 128 + HALF * h + c, a, b);
         else tmem_ld16(tb + HALF * h + c, a);
         float v[16];
@@ -452,6 +453,7 @@ __device__ __forceinline__ void short_plain(const KP& p, const Item& it, uint32_
         const int c = 32 * h + (i & 16) + (i & ~31) * 2;
         if (c >= it.n) continue;
         uint32_t v[16];
+        __syncwarp();
         tmem_ld16(tb + c, v);
         float y[16];
 #pragma unroll
@@ -473,6 +475,7 @@ __device__ __forceinline__ void short_swiglu(const KP& p, const Item& it, uint32
         const int c = 32 * h + (i & 16) + (i & ~31) * 2;
         if (c >= it.n) continue;
         uint32_t v[16];
+        __syncwarp();
         tmem_ld16(tb + c, v);
         float keep[8], y[8];
 #pragma unroll
@@ -747,7 +750,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             for (int v = 0; v < 4; ++v) scales[32 * v + lane] = nx.sc[v];
             __syncwarp();
             more = fetch();
-            const bool ok = wait_i8(&ctl->tfull[acc], aph, ctl, p, peer_abort);
+            const bool ok = __all_sync(0xffffffffu, wait_i8(&ctl->tfull[acc], aph, ctl, p, peer_abort));   // one answer a warp
             aph ^= 1u;
             // The warps of a pair leave together, so that neither waits for the other: on the word of both at a
             // short tile, else after the loop, where one that has left early answers the other's last question.
@@ -772,9 +775,11 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 else mbar_arrive_remote(tempty0);
             }
         }
+        __syncwarp();
         if (SWIGLU && !met) pair_and(pid, false);
         if (lane == 0) bulk_wait_all();
     }
+    __syncwarp();
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
@@ -1020,7 +1025,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             __syncwarp();
             i += 2;
             fetch(i);
-            if (!wait_i8(&ctl->tfull[acc], aph, ctl, p)) break;
+            if (!__all_sync(0xffffffffu, wait_i8(&ctl->tfull[acc], aph, ctl, p))) break;   // one answer a warp
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * ACC_COLS);
             int* sums = p.part + static_cast<size_t>(w.tail) * 256 * p.part_rows + r;   // [row][256 channels]
@@ -1028,6 +1033,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 #pragma unroll 1
                 for (int c = 16 * h; c < nrow; c += 16 * H) {
                     uint32_t lo[16], hi[16];
+                    __syncwarp();
                     tmem_ld16x2(tb + c, tb + 128 + c, lo, hi);
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
@@ -1047,6 +1053,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 #pragma unroll 1
             for (int c = 16 * h; c < nrow; c += 16 * H) {
                 uint32_t lo[16], hi[16];
+                __syncwarp();
                 if (w.parts == 1) {
                     tmem_ld16x2(tb + c, tb + 128 + c, lo, hi);
                 } else {
@@ -1085,6 +1092,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             aph ^= 1u;
         }
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
