@@ -12,8 +12,10 @@
 // read the accumulators back (tcgen05.ld), apply the scales and store: half of
 // them to each of the two accumulators, which the tiles take in turn. The tile
 // list is formed in each CTA's shared memory from the group offsets. Every wait
-// is bounded (moe_set_wait_limit): on expiry the CTA records MOE_ERR_TIMEOUT,
-// lets what it started land, frees its tensor memory and returns.
+// is bounded (moe_set_wait_limit): on expiry the CTA records MOE_ERR_TIMEOUT and
+// its warps leave their loops. One that had come to its end before may have left
+// copies or MMAs behind that the others no longer wait for, so what was started
+// lands after all warps have met: then the CTA frees its tensor memory and returns.
 //  * pair: clusters of two CTAs share tiles of 256 rows of A x 512 weight
 //    rows (cta_group::2), each CTA loading half of both; groups of many rows.
 //    Bound by the tensor pipe and the board's power: 8192 rows, K = 14336,
@@ -88,6 +90,7 @@ struct Ctl {
     uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
+    uint32_t loaded;          // K blocks that the CTA has requested, written as its loads end
     int cum[MOE_MAX_E + 1];   // tiles before group g
     int row0[MOE_MAX_E + 1];  // first row of group g
     int most;                 // rows of the tallest tile
@@ -187,7 +190,7 @@ __device__ __forceinline__ bool wait_i8(uint64_t* bar, uint32_t parity, C* ctl, 
         }
     }
 }
-// On the abort path: copies and MMAs in flight land before the CTA leaves.
+// After a wait gave up: copies and MMAs in flight land before the CTA leaves.
 __device__ __forceinline__ void drain_i8(uint64_t* bar, uint32_t parity, const KP& p) {
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(bar, parity))
@@ -195,6 +198,20 @@ __device__ __forceinline__ void drain_i8(uint64_t* bar, uint32_t parity, const K
             atomicExch(p.status, MOE_ERR_TIMEOUT);
             return;
         }
+}
+
+// The last requests of every stage: block j of `n` completes phase (j / STAGES) % 2 of full[j % STAGES].
+template <int STAGES>
+__device__ __forceinline__ void drain_loads(Ctl<STAGES>* ctl, uint32_t n, const KP& p) {
+    for (uint32_t j = n > STAGES ? n - STAGES : 0; j < n; ++j) drain_i8(&ctl->full[j % STAGES], (j / STAGES) & 1u, p);
+}
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_remote_u32(uint32_t cluster_addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    return v;
 }
 
 // ---- epilogue arithmetic -------------------------------------------------------
@@ -549,11 +566,16 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int num_kb = (p.K + BKB - 1) / BKB;
     constexpr int SET = SWIGLU ? 128 : 256;   // channels of one of a tile's two sets
     auto sets_of = [&](const Item& it) { return it.t.n_blk * 2 * SET + SET < p.N ? 2 : 1; };
+    auto boxes_of = [&](const Item& it) { return it.shrt ? ((it.n + 31) / 32 * 16 + 31) / 32 : 0; };
+    // bytes of a K block that each of the two CTAs loads
+    auto tx_of = [&](const Item& it) -> uint32_t {
+        return (it.shrt ? boxes_of(it) * 32 * BKB : A_BYTES) + sets_of(it) * BH_BYTES;
+    };
 
     if (warp == 0) {
         if (lane == 0) {
             int s = 0;
-            uint32_t ph = 0, armed = 0, armed_ph = 0;
+            uint32_t ph = 0, loaded = 0;
             bool aborted = false;
             auto full_of = [&](int st) { return mapa_shared(smem_u32(&ctl->full[st]), 0u); };
             for (int u = cluster; u < work.items && !aborted; u += nclusters) {
@@ -563,21 +585,17 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 // this rank's rows of A: 128 in one box, or of a short tile half of its N columns in boxes of 32
                 const int half_n = (it.n + 31) / 32 * 16;
                 const int arow = static_cast<int>(it.row0) + rank * (it.shrt ? half_n : BM);
-                const int boxes = it.shrt ? (half_n + 31) / 32 : 0;
+                const int boxes = boxes_of(it);
                 // its two 64-row boxes of weights of each set
                 const int b0 = it.t.g * p.N + it.t.n_blk * 2 * SET + (SWIGLU ? (it.shrt ? rank * 64 : 0) : rank * 128);
                 const int b1 = SWIGLU && it.shrt ? b0 : b0 + 64;
                 const CUtensorMap* m0 = SWIGLU && !it.shrt && rank ? &tmB1 : &tmB0;
                 const CUtensorMap* m1 = SWIGLU && it.shrt ? &tmB1 : m0;
-                const uint32_t bytes = (it.shrt ? boxes * 32 * BKB : A_BYTES) + sets * BH_BYTES;
+                const uint32_t bytes = tx_of(it);
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (!wait_i8(&ctl->empty[s], ph ^ 1u, ctl, p, peer_abort)) { aborted = true; break; }
                     const uint32_t sa = smem_u32(smem + s * P_STAGE_BYTES);
-                    if (leader) {
-                        mbar_arrive_expect_tx(&ctl->full[s], 2 * bytes);
-                        armed |= 1u << s;
-                        armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
-                    }
+                    if (leader) mbar_arrive_expect_tx(&ctl->full[s], 2 * bytes);
                     if (it.shrt) {
                         for (int q = 0; q < boxes; ++q)
                             tma_load_2d_pair(sa + q * 32 * BKB, &tmA32, full_of(s), kb * BKB, arow + 32 * q);
@@ -589,25 +607,17 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         tma_load_2d_pair(sw, m0, full_of(s), kb * BKB, b0 + z * SET);
                         tma_load_2d_pair(sw + BH_BYTES / 2, m1, full_of(s), kb * BKB, b1 + z * SET);
                     }
+                    ++loaded;
                     if (++s == P_STAGES) { s = 0; ph ^= 1u; }
                 }
             }
-            if (aborted) {
-                if (leader) {
-                    for (int st = 0; st < P_STAGES; ++st)
-                        if ((armed >> st) & 1u) drain_i8(&ctl->full[st], (armed_ph >> st) & 1u, p);
-                } else {
-                    // its own copies complete on the leader's barriers: a fixed time for them to land
-                    const uint64_t t0 = global_timer_ns();
-                    while (global_timer_ns() - t0 < 50000ull) {}
-                }
-            }
+            ctl->loaded = loaded;
         }
     } else if (warp == 1) {
         if (lane == 0 && leader) {
             int s = 0;
             uint32_t ph = 0, aph[2] = {0u, 0u}, first_acc = 0;   // the accumulators take the sets in turn
-            bool aborted = false, issued = false;
+            bool aborted = false;
             for (int u = cluster; u < work.items && !aborted; u += nclusters) {
                 const Item it = item_at(ctl, p, work, u);
                 if (it.n == 0) continue;
@@ -625,7 +635,6 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
                         for (int kk = 0; kk < BKB / 32; ++kk)
                             mma_i8_pair(d, md + 2u * kk, nd + 2u * kk, id, (kb + i) | kk ? 1u : 0u);
-                        issued = true;
                         if (z == sets - 1) tc_commit_pair_mc(&ctl->empty[st], 0x3);
                         if (++st == P_STAGES) { st = 0; p0 ^= 1u; }
                     }
@@ -665,10 +674,6 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 if (ok && sets == 2) full_acc(1);
                 first_acc += sets;
                 aborted = !ok;
-            }
-            if (aborted && issued) {
-                tc_commit_pair(&ctl->drain);
-                drain_i8(&ctl->drain, 0, p);
             }
         }
     } else {
@@ -783,6 +788,34 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
+    // A wait gave up (both CTAs carry the flag): the leader's barriers count both CTAs' copies, so it
+    // waits for all of them. Where one CTA has requested more blocks than the other, the bytes that will
+    // not come are taken off the leader's phase, or the phase is armed for the other CTA's alone.
+    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) {
+        if (leader && threadIdx.x == 0) {
+            const uint32_t n0 = ctl->loaded, n1 = ld_shared_remote_u32(mapa_shared(smem_u32(&ctl->loaded), 1u));
+            uint32_t j = 0;   // blocks up to the end of the item
+            const uint32_t lo = min(n0, n1), hi = max(n0, n1);
+            for (int u = cluster; u < work.items && j < hi; u += nclusters) {
+                const Item it = item_at(ctl, p, work, u);
+                if (it.n == 0) continue;
+                const uint32_t from = max(j, lo), to = min(j + num_kb, hi);
+                for (uint32_t b = from; b < to; ++b) {
+                    if (n0 > n1) mbar_complete_tx(&ctl->full[b % P_STAGES], tx_of(it));
+                    else mbar_arrive_expect_tx(&ctl->full[b % P_STAGES], tx_of(it));
+                }
+                j += num_kb;
+            }
+            drain_loads(ctl, hi, p);
+        } else if (leader && threadIdx.x == 32) {
+            tc_commit_pair(&ctl->drain);
+            drain_i8(&ctl->drain, 0, p);
+        }
+        __syncwarp();
+        tc_fence_before();
+        cluster_sync_all();
+        tc_fence_after();
+    }
     if (warp == 1) {
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
@@ -911,7 +944,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     if (warp == 0) {
         if (lane == 0) {
             int s = 0;
-            uint32_t ph = 0, armed = 0, armed_ph = 0;
+            uint32_t ph = 0, loaded = 0;
             bool aborted = false;
             Unit w;
             for (int i = 0; !aborted && unit_at(un, b, i, w); ++i) {
@@ -931,24 +964,21 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     if (!wait_i8(&ctl->empty[s], ph ^ 1u, ctl, p)) { aborted = true; break; }
                     const uint32_t sa = smem_u32(smem + s * S_STAGE_BYTES);
                     mbar_arrive_expect_tx(&ctl->full[s], bytes);
-                    armed |= 1u << s;
-                    armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
                     tma_load_2d(sa + A_BYTES, m0, &ctl->full[s], kb * BKB, brow);
                     if (two) tma_load_2d(sa + A_BYTES + BH_BYTES, m1, &ctl->full[s], kb * BKB, brow1);
                     for (int q = 0; q < boxes; ++q)
                         tma_load_2d(sa + q * 32 * BKB, &tmA, &ctl->full[s], kb * BKB, arow + 32 * q);
+                    ++loaded;
                     if (++s == S_STAGES) { s = 0; ph ^= 1u; }
                 }
             }
-            if (aborted)
-                for (int st = 0; st < S_STAGES; ++st)
-                    if ((armed >> st) & 1u) drain_i8(&ctl->full[st], (armed_ph >> st) & 1u, p);
+            ctl->loaded = loaded;
         }
     } else if (warp == 1) {
         if (lane == 0) {
             int s = 0, acc = 0;
             uint32_t ph = 0, aph = 0;
-            bool aborted = false, issued = false;
+            bool aborted = false;
             Unit w;
             for (int i = 0; !aborted && unit_at(un, b, i, w); ++i) {
                 const Tile t = tile_of(ctl, p, w.tile, BM);
@@ -968,7 +998,6 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         mma_i8(d, w0 + 2u * kk, xd + 2u * kk, id, accum);
                         if (two) mma_i8(d + 128u, w1 + 2u * kk, xd + 2u * kk, id, accum);
                     }
-                    issued = true;
                     tc_commit(&ctl->empty[s]);
                     if (++s == S_STAGES) { s = 0; ph ^= 1u; }
                 }
@@ -976,10 +1005,6 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 tc_commit(&ctl->tfull[acc]);
                 acc ^= 1;
                 if (acc == 0) aph ^= 1u;
-            }
-            if (aborted && issued) {
-                tc_commit(&ctl->drain);
-                drain_i8(&ctl->drain, 0, p);
             }
         }
     } else {
@@ -1096,6 +1121,18 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) {   // a wait gave up
+        if (threadIdx.x == 0) {
+            drain_loads(ctl, ctl->loaded, p);
+        } else if (threadIdx.x == 32) {
+            tc_commit(&ctl->drain);
+            drain_i8(&ctl->drain, 0, p);
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
     if (warp == 1) {
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
