@@ -111,6 +111,7 @@ struct Ctl {
     uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
+    uint32_t loaded;   // K blocks requested, written as the loads end
 };
 
 __device__ __forceinline__ bool wait_b(uint64_t* bar, uint32_t parity, Ctl* ctl, const BParams& p) {
@@ -230,7 +231,7 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
         // ---------------- TMA producer ----------------
         if (lane == 0) {
             int s = 0;
-            uint32_t ph = 0, issued_mask = 0, issued_ph = 0;
+            uint32_t ph = 0, loaded = 0;
             bool aborted = false;
             for (int u = blockIdx.x; u < units && !aborted; u += gridDim.x) {
                 const BTile t = decode<MODE>(p, u);
@@ -239,14 +240,11 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
                     mbar_arrive_expect_tx(&ctl->full[s], STAGE_BYTES);
                     issue_stage<MODE>(p, t, kb, smem_u32(smem + s * STAGE_BYTES), &ctl->full[s], &mA, &mB0, &mB1,
                                       true, true);
-                    issued_mask |= 1u << s;
-                    issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+                    ++loaded;
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
             }
-            if (aborted)
-                for (int st = 0; st < STAGES; ++st)
-                    if ((issued_mask >> st) & 1u) wait_d(&ctl->full[st], (issued_ph >> st) & 1u, p);
+            ctl->loaded = loaded;
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
@@ -254,7 +252,7 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
             constexpr uint32_t idesc = make_idesc_major(BM, BN, A_MN ? 1 : 0, 1);
             int s = 0, acc = 0;
             uint32_t ph = 0, aph = 0;
-            bool aborted = false, issued_any = false;
+            bool aborted = false;
             for (int u = blockIdx.x; u < units && !aborted; u += gridDim.x) {
                 const BTile t = decode<MODE>(p, u);
                 if (!wait_b(&ctl->tempty[acc], aph ^ 1u, ctl, p)) { aborted = true; break; }
@@ -274,7 +272,6 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
                         const uint64_t bd = b0 + static_cast<uint64_t>(kk) * (2048 >> 4);
                         tc_mma(d_tmem, ad, bd, idesc, (kb != 0 || kk != 0) ? 1u : 0u);
                     }
-                    issued_any = true;
                     tc_commit(&ctl->empty[s]);
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
@@ -282,10 +279,6 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
                 tc_commit(&ctl->tfull[acc]);   // with no K-block this arrives at once
                 acc ^= 1;
                 if (acc == 0) aph ^= 1u;
-            }
-            if (aborted && issued_any) {
-                tc_commit(&ctl->drain);
-                wait_d(&ctl->drain, 0, p);
             }
         }
     } else {
@@ -441,6 +434,19 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) {   // a wait gave up: what was started lands
+        if (threadIdx.x == 0) {
+            for (uint32_t j = ctl->loaded > STAGES ? ctl->loaded - STAGES : 0; j < ctl->loaded; ++j)
+                wait_d(&ctl->full[j % STAGES], (j / STAGES) & 1u, p);
+        } else if (threadIdx.x == 32) {
+            tc_commit(&ctl->drain);
+            wait_d(&ctl->drain, 0, p);
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
     if (warp == 1) {
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)

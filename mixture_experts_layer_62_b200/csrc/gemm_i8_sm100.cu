@@ -205,14 +205,6 @@ template <int STAGES>
 __device__ __forceinline__ void drain_loads(Ctl<STAGES>* ctl, uint32_t n, const KP& p) {
     for (uint32_t j = n > STAGES ? n - STAGES : 0; j < n; ++j) drain_i8(&ctl->full[j % STAGES], (j / STAGES) & 1u, p);
 }
-__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
-    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ uint32_t ld_shared_remote_u32(uint32_t cluster_addr) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
-    return v;
-}
 
 // ---- epilogue arithmetic -------------------------------------------------------
 // Two fp32 values an instruction (f32x2: each rounded as the scalar form).

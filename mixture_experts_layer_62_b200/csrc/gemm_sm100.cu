@@ -27,8 +27,9 @@
 //    the ragged tail of a group, conversion and 16-byte stores; the next
 //    tile's MMAs run into the other accumulator meanwhile.
 //  * every mbarrier wait is bounded by a wall-clock limit; on expiry the CTA
-//    records MOE_ERR_TIMEOUT, drains its in-flight TMA and MMA work, frees
-//    TMEM and returns.
+//    records MOE_ERR_TIMEOUT, its warps leave their loops and meet, the TMA and
+//    MMA work in flight (of whichever warp) is drained, TMEM is freed and the
+//    CTA returns.
 // No cluster multicast anywhere: every CTA fetches its own tiles.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -196,6 +197,7 @@ struct SharedCtl {
     uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
+    uint32_t loaded;   // K blocks requested, written as the loads end
 };
 
 // Wait for phase `parity` of `bar`; false if the CTA aborted or the limit ran out.
@@ -213,7 +215,7 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, Sha
         }
     }
 }
-// Drain wait used on the abort path: ignores the abort flag and has a limit
+// Drain wait used after a wait gave up: ignores the abort flag and has a limit
 // of its own, long, so that a short wait limit never cuts a drain short.
 __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, const KParams& p) {
     const uint64_t t0 = global_timer_ns();
@@ -394,8 +396,7 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
         // ---------------- TMA producer ----------------
         if (lane == 0) {
             int s = 0;
-            uint32_t ph = 0;
-            uint32_t issued_mask = 0, issued_ph = 0;
+            uint32_t ph = 0, loaded = 0;
             bool aborted = false;
             int pre = 0;   // stages of the first unit whose weight tiles were requested before the wait
             // the unit's tile and K-block range (a split of it with split-K)
@@ -451,7 +452,6 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
                         const uint32_t sa = smem_u32(smem + pre * STAGE_BYTES);
                         mbar_arrive_expect_tx(&ctl->full[pre], stage_tx(t));
                         load_b(sa, l, kb, &ctl->full[pre]);
-                        issued_mask |= 1u << pre;
                     }
                 }
                 pdl_wait();
@@ -472,18 +472,13 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
                         load_a(sa, t, l, kb, &ctl->full[s]);
                         load_b(sa, l, kb, &ctl->full[s]);
                     }
-                    issued_mask |= 1u << s;
-                    issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+                    ++loaded;
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
             }
-            if (aborted) {
-                // let every load this thread started land before the CTA exits
-                // (the stages requested before the wait got their A rows before
-                // any wait could give up, so their barriers complete too)
-                for (int st = 0; st < STAGES; ++st)
-                    if ((issued_mask >> st) & 1u) wait_drain(&ctl->full[st], (issued_ph >> st) & 1u, p);
-            }
+            // (the stages requested before the dependency wait got their A rows
+            // before any wait could give up, so they are counted)
+            ctl->loaded = loaded;
         } else if (early) {
             pdl_wait();
             pdl_launch();
@@ -500,7 +495,7 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
             uint32_t ph = 0;
             int acc = 0;
             uint32_t aph = 0;
-            bool aborted = false, issued_any = false;
+            bool aborted = false;
             for (int u = un.first; u < un.count && !aborted; u += un.step) {
                 int kb0 = 0, kb1;
                 Tile t;
@@ -542,7 +537,6 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
                         for (int kk = 0; kk < BK / 16; ++kk)
                             tc_mma(d_tmem, adesc + 2u * kk, bdesc + 2u * kk, idesc, (kb != kb0 || kk != 0) ? 1u : 0u);
                     }
-                    issued_any = true;
                     tc_commit(&ctl->empty[s]);
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
@@ -550,11 +544,6 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
                 tc_commit(&ctl->tfull[acc]);
                 acc ^= 1;
                 if (acc == 0) aph ^= 1u;
-            }
-            if (aborted && issued_any) {
-                // all MMAs of this thread must finish before TMEM is freed
-                tc_commit(&ctl->drain);
-                wait_drain(&ctl->drain, 0, p);
             }
         }
     } else {
@@ -721,6 +710,19 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) {   // a wait gave up: what was started lands
+        if (threadIdx.x == 0) {
+            for (uint32_t j = ctl->loaded > STAGES ? ctl->loaded - STAGES : 0; j < ctl->loaded; ++j)
+                wait_drain(&ctl->full[j % STAGES], (j / STAGES) & 1u, p);
+        } else if (threadIdx.x == 32) {
+            tc_commit(&ctl->drain);
+            wait_drain(&ctl->drain, 0, p);
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
     if (warp == 1) {
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
@@ -759,6 +761,7 @@ struct PairCtl {
     uint64_t full[P_STAGES], empty[P_STAGES], tfull[2], tempty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
+    uint32_t loaded;   // K blocks this CTA has requested, written as its loads end
 };
 
 __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, PairCtl* ctl, uint32_t peer_abort,
@@ -952,8 +955,7 @@ tc_pair_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ C
         // ---------------- TMA producer (both CTAs) ----------------
         if (lane == 0) {
             int s = 0;
-            uint32_t ph = 0;
-            uint32_t armed_mask = 0, armed_ph = 0;   // leader: stages whose full barrier it armed
+            uint32_t ph = 0, loaded = 0;
             bool aborted = false;
             int pre = 0;
             const CUtensorMap* mbh[2] = {MODE == TC_SWIGLU && rank ? &tmB01 : &tmB00,
@@ -970,10 +972,7 @@ tc_pair_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ C
                     const int brow = b_row(t);
                     for (int kb = 0; kb < t.num_kb && pre < P_STAGES; ++kb, ++pre) {
                         const uint32_t sa = smem_u32(smem + pre * P_STAGE_BYTES);
-                        if (leader) {
-                            mbar_arrive_expect_tx(&ctl->full[pre], 2 * P_STAGE_BYTES);
-                            armed_mask |= 1u << pre;
-                        }
+                        if (leader) mbar_arrive_expect_tx(&ctl->full[pre], 2 * P_STAGE_BYTES);
                         tma_load_2d_pair(sa + A_BYTES, mbh[t.kind], full_of(pre), kb * BK, brow);
                     }
                 }
@@ -992,29 +991,15 @@ tc_pair_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ C
                         tma_load_2d_pair(sa, ma, full_of(s), kb * BK, arow);
                     } else {
                         if (!pair_wait(&ctl->empty[s], ph ^ 1u, ctl, peer_abort, p)) { aborted = true; break; }
-                        if (leader) {
-                            mbar_arrive_expect_tx(&ctl->full[s], 2 * P_STAGE_BYTES);
-                            armed_mask |= 1u << s;
-                            armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
-                        }
+                        if (leader) mbar_arrive_expect_tx(&ctl->full[s], 2 * P_STAGE_BYTES);
                         tma_load_2d_pair(sa, ma, full_of(s), kb * BK, arow);
                         tma_load_2d_pair(sa + A_BYTES, mbh[t.kind], full_of(s), kb * BK, brow);
                     }
+                    ++loaded;
                     if (++s == P_STAGES) { s = 0; ph ^= 1u; }
                 }
             }
-            if (aborted) {
-                // the leader's armed stages complete when both CTAs' bytes have
-                // landed; a load of the other CTA's that no armed phase counts
-                // is given a fixed time to land (it cannot be observed here)
-                if (leader) {
-                    for (int st = 0; st < P_STAGES; ++st)
-                        if ((armed_mask >> st) & 1u) wait_drain(&ctl->full[st], (armed_ph >> st) & 1u, p);
-                } else {
-                    const uint64_t t0 = global_timer_ns();
-                    while (global_timer_ns() - t0 < 50000ull) {}
-                }
-            }
+            ctl->loaded = loaded;
         } else if (early) {
             pdl_wait();
             pdl_launch();
@@ -1031,7 +1016,7 @@ tc_pair_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ C
             uint32_t ph = 0;
             int acc = 0;
             uint32_t aph = 0;
-            bool aborted = false, issued_any = false;
+            bool aborted = false;
             constexpr uint32_t idesc_half = make_idesc(PBM, 128);
             for (int u = cluster; u < work.items && !aborted; u += nclusters) {
                 int hf;
@@ -1051,7 +1036,6 @@ tc_pair_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ C
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
                         tc_mma_pair(d_tmem, adesc + 2u * kk, bdesc + 2u * kk, id, (kb | kk) != 0 ? 1u : 0u);
-                    issued_any = true;
                     tc_commit_pair_mc(&ctl->empty[s], 0x3);
                     if (++s == P_STAGES) { s = 0; ph ^= 1u; }
                 }
@@ -1059,12 +1043,6 @@ tc_pair_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ C
                 tc_commit_pair_mc(&ctl->tfull[acc], 0x3);
                 acc ^= 1;
                 if (acc == 0) aph ^= 1u;
-            }
-            if (aborted && issued_any) {
-                // every MMA of this thread (both CTAs' memories) must finish
-                // before either CTA frees its tensor memory
-                tc_commit_pair(&ctl->drain);
-                wait_drain(&ctl->drain, 0, p);
             }
         }
     } else {
@@ -1110,6 +1088,29 @@ tc_pair_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ C
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
+    // A wait gave up (both CTAs carry the flag): what was started lands. The
+    // leader's barriers count both CTAs' bytes; where one has requested more
+    // blocks than the other, the bytes that will not come are taken off the
+    // leader's phase, or the phase is armed for the other CTA's alone.
+    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) {
+        if (leader && threadIdx.x == 0) {
+            const uint32_t n0 = ctl->loaded, n1 = ld_shared_remote_u32(mapa_shared(smem_u32(&ctl->loaded), 1u));
+            const uint32_t hi = max(n0, n1);
+            for (uint32_t j = min(n0, n1); j < hi; ++j) {
+                if (n0 > n1) mbar_complete_tx(&ctl->full[j % P_STAGES], P_STAGE_BYTES);
+                else mbar_arrive_expect_tx(&ctl->full[j % P_STAGES], P_STAGE_BYTES);
+            }
+            for (uint32_t j = hi > P_STAGES ? hi - P_STAGES : 0; j < hi; ++j)
+                wait_drain(&ctl->full[j % P_STAGES], (j / P_STAGES) & 1u, p);
+        } else if (leader && threadIdx.x == 32) {
+            tc_commit_pair(&ctl->drain);
+            wait_drain(&ctl->drain, 0, p);
+        }
+        __syncwarp();
+        tc_fence_before();
+        cluster_sync_all();
+        tc_fence_after();
+    }
     if (warp == 1) {
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)

@@ -1,0 +1,97 @@
+"""A wait of the bf16 tensor-core kernels that gives up at any point of a
+launch: limits from one probe to several microseconds stop the loads, the MMAs
+and the epilogues at different places, also where one of them has come to its
+end already and the two CTAs of a pair have requested different numbers of
+blocks. What was started lands before a CTA leaves, without the two seconds
+after which even that is given up, and the next call gives the same bits as
+before."""
+
+import math
+import time
+
+import pytest
+import torch
+
+import mixture_experts_layer_62_b200 as moe
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+LIMITS = (1, 200, 700, 1500, 3000, 6000, 12000, 25000)
+
+
+def randn(g, *shape):
+    return (torch.randn(shape, generator=g, device=DEV) / math.sqrt(shape[-1])).to(torch.bfloat16)
+
+
+def sweep(call, names):
+    """call() -> (outputs, status); names: how the outputs are called."""
+    def timed():
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        out, status = call()
+        torch.cuda.synchronize()
+        return out, status(), time.perf_counter() - t0
+
+    right, status, _ = timed()
+    assert status == moe.MOE_OK
+    for limit in LIMITS:
+        prev = moe.set_wait_limit(limit)
+        try:
+            for _ in range(3):
+                out, status, seconds = timed()
+                same = all(torch.equal(a, b) for a, b in zip(out, right))
+                assert status == moe.MOE_ERR_TIMEOUT or (status == moe.MOE_OK and same and limit > 1)
+                assert seconds < 1.0
+        finally:
+            moe.set_wait_limit(prev)
+        out, status, _ = timed()
+        assert status == moe.MOE_OK
+        for name, a, b in zip(names, out, right):
+            assert torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("T,d,dff,E,form", [
+    (400, 256, 384, 4, "single"),       # K blocks of a tile: no more than stages
+    (800, 2048, 1024, 4, "single"),
+    (12, 1024, 2048, 4, "split_k"),
+    (2100, 256, 512, 2, "pair"),
+    (2100, 4096, 2048, 2, "pair"),
+])
+def test_experts(T, d, dff, E, form):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T + d)
+    p = moe.problem(T, d, dff, E, 1)
+    assert moe.gemm_variant(p) == form
+    xp, W1, W3, W2 = randn(g, T, d), randn(g, E, dff, d), randn(g, E, dff, d), randn(g, E, d, dff)
+    ends = torch.linspace(0, T, E + 1).to(torch.int32).to(DEV)
+    work = moe.alloc_workspace(p, DEV)
+
+    def call():
+        st, o = moe.alloc_stats(E, DEV), torch.zeros((T, d), dtype=torch.bfloat16, device=DEV)
+        moe.experts(p, xp, ends, W1, W3, W2, o, work, stats=st)
+        return (o,), lambda: moe.read_stats(st, E).status
+
+    sweep(call, ("o",))
+
+
+@pytest.mark.parametrize("T,d,dff", [(300, 256, 256), (1500, 1024, 512)])
+def test_backward(T, d, dff):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    E, k = 8, 2
+    p = moe.problem(T, d, dff, E, k, pad_rows=64, train=1)
+    x, dy, W_r = randn(g, T, d) * 8, randn(g, T, d), randn(g, d, E)
+    W1, W3, W2 = randn(g, E, dff, d), randn(g, E, dff, d), randn(g, E, d, dff)
+    ws, bws = moe.alloc_workspace(p, DEV), moe.alloc_backward_workspace(p, DEV)
+    out = torch.empty((T, d), dtype=torch.bfloat16, device=DEV)
+
+    def call():
+        limit = moe.set_wait_limit(0)
+        st = moe.alloc_stats(E, DEV)
+        moe.forward(p, x, W_r, W1, W3, W2, out, st, ws)
+        moe.set_wait_limit(limit)
+        grads = [torch.empty_like(x)] + [torch.empty(w.shape, device=DEV) for w in (W_r, W1, W3, W2)]
+        moe.backward(p, x, W_r, W1, W3, W2, dy, *grads, st, ws, bws)
+        return grads, lambda: moe.read_stats(st, E).status
+
+    sweep(call, ("dx", "dW_r", "dW1", "dW3", "dW2"))
