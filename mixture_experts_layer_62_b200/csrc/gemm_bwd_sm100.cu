@@ -310,7 +310,7 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
 #pragma unroll
                     for (int i = 0; i < 4; ++i) { na[i] = pa[i]; nb[i] = pa[16 + i]; }
                 }
-                if (!wait_b(&ctl->tfull[acc], aph, ctl, p)) break;
+                if (!__all_sync(0xffffffffu, wait_b(&ctl->tfull[acc], aph, ctl, p))) break;   // one answer a warp
                 tc_fence_after();
                 const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                     static_cast<uint32_t>(acc * ACC_COLS);
@@ -325,6 +325,7 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
                         for (int i = 0; i < 4; ++i) { na[i] = pa[i]; nb[i] = pa[16 + i]; }
                     }
                     uint32_t v[32];
+                    __syncwarp();   // the load is the warp's: all lanes come to it together
                     tmem_ld32(tb + c, v);
                     if (chunk_ok(c)) {
                         uint4* qa = reinterpret_cast<uint4*>(p.out_bf16 + chunk_off(c));
@@ -354,7 +355,7 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
                     }
                 }
             } else if (MODE == BW_DX) {
-                if (!wait_b(&ctl->tfull[acc], aph, ctl, p)) break;
+                if (!__all_sync(0xffffffffu, wait_b(&ctl->tfull[acc], aph, ctl, p))) break;   // one answer a warp
                 tc_fence_after();
                 const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                     static_cast<uint32_t>(acc * ACC_COLS);
@@ -365,6 +366,7 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
 #pragma unroll 1
                 for (int c = 0; c < BN; c += 32) {
                     uint32_t v[32];
+                    __syncwarp();   // the load is the warp's: all lanes come to it together
                     tmem_ld32(tb + c, v);
                     const int col = t.n_blk * BN + c;
                     if (valid && col < p.N) {
@@ -384,7 +386,7 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
                 // the 128-byte-swizzled layout of the output map and stored by
                 // one bulk tensor store; two buffers per warp let the next block
                 // be written while the previous store still reads.
-                if (!wait_b(&ctl->tfull[acc], aph, ctl, p)) break;
+                if (!__all_sync(0xffffffffu, wait_b(&ctl->tfull[acc], aph, ctl, p))) break;   // one answer a warp
                 tc_fence_after();
                 const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                     static_cast<uint32_t>(acc * ACC_COLS);
@@ -401,6 +403,7 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
 #pragma unroll 1
                 for (int c = 0; c < BN; c += 32) {
                     uint32_t v[32];
+                    __syncwarp();   // the load is the warp's: all lanes come to it together
                     if (!empty_k) tmem_ld32(tb + c, v);
                     const int col = t.n_blk * BN + c;
                     if (col >= p.N) continue;          // the same for the whole warp

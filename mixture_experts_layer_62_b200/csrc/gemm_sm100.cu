@@ -561,7 +561,7 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
             bool cs;
             const Tile t = un.small ? decode_small_tile(p, u)
                          : (p.split_grid && p.interleave) ? decode_mixed(p, u, cs) : decode_tile(p, u / nsplit);
-            if (!wait_bounded(&ctl->tfull[acc], aph, ctl, p)) break;
+            if (!__all_sync(0xffffffffu, wait_bounded(&ctl->tfull[acc], aph, ctl, p))) break;   // one answer a warp
             tc_fence_after();
             const int grow = t.m_blk * BM + r;
             bool valid = grow < t.rows;
@@ -583,6 +583,7 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
 #pragma unroll 1
                 for (int c = 0; c < ncol; c += 32) {
                     uint32_t v0[32], v1[32];
+                    __syncwarp();   // the load is the warp's: all lanes come to it together
                     tmem_ld32(tb + c, v0);
                     tmem_ld32(tb + 128 + c, v1);
 #pragma unroll
@@ -606,6 +607,7 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
 #pragma unroll 1
                 for (int c = 0; c < 256; c += 32) {
                     uint32_t v[32];
+                    __syncwarp();   // the load is the warp's: all lanes come to it together
                     tmem_ld32(tb + c, v);
                     const int col = t.n_blk * 256 + c;
                     if (valid && col < p.partial_ld) {
@@ -632,6 +634,7 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
 #pragma unroll 1
                 for (int c = 0; c < 128; c += 32) {
                     uint32_t gv[32], uv[32];
+                    __syncwarp();   // the load is the warp's: all lanes come to it together
                     tmem_ld32(tb + c, gv);
                     tmem_ld32(tb + 128 + c, uv);
                     const int col = t.n_blk * 128 + c;
@@ -669,6 +672,7 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
 #pragma unroll 1
                 for (int c = 0; c < 256; c += 32) {
                     uint32_t v[32];
+                    __syncwarp();   // the load is the warp's: all lanes come to it together
                     tmem_ld32(tb + c, v);
                     const int col = t.n_blk * 256 + c;
                     if (valid && col < N) {
@@ -687,6 +691,7 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
 #pragma unroll 1
                 for (int c = 0; c < 256; c += 32) {
                     uint32_t v[32];
+                    __syncwarp();   // the load is the warp's: all lanes come to it together
                     tmem_ld32(tb + c, v);
                     const int col = t.n_blk * 256 + c;
                     if (valid && col < N) {
@@ -792,6 +797,7 @@ __device__ __forceinline__ void pair_store_row(const KParams& p, const Tile& t, 
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
             uint32_t gv[32], uv[32];
+            __syncwarp();   // the load is the warp's: all lanes come to it together
             tmem_ld32(tb + c, gv);
             tmem_ld32(tb + 128 + c, uv);
             const int col = t.n_blk * 128 + c;
@@ -814,6 +820,7 @@ __device__ __forceinline__ void pair_store_row(const KParams& p, const Tile& t, 
 #pragma unroll 1
         for (int c = 0; c < 256; c += 32) {
             uint32_t v[32];
+            __syncwarp();   // the load is the warp's: all lanes come to it together
             tmem_ld32(tb + c, v);
             const int col = t.n_blk * 256 + c;
             if (valid && col < N) {
@@ -843,6 +850,7 @@ __device__ __forceinline__ void pair_store_half_row(const KParams& p, const Tile
 #pragma unroll 1
     for (int c = 0; c < 64; c += 32) {
         uint32_t lo[32], hi[32];
+        __syncwarp();   // the load is the warp's: all lanes come to it together
         tmem_ld32(tb + c, lo);
         tmem_ld32(tb + 64 + c, hi);
         if (!valid) continue;
@@ -1060,7 +1068,7 @@ tc_pair_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ C
         for (int u = cluster; u < work.items; u += nclusters) {
             int hf;
             const Tile t = decode_tile_m<PBM>(p, pair_item_tile(work, u, hf));
-            if (!pair_wait(&ctl->tfull[acc], aph, ctl, peer_abort, p)) break;
+            if (!__all_sync(0xffffffffu, pair_wait(&ctl->tfull[acc], aph, ctl, peer_abort, p))) break;   // one answer a warp
             tc_fence_after();
             const int grow = t.m_blk * PBM + r;
             const size_t orow = static_cast<size_t>(t.row0) + static_cast<size_t>(grow);
