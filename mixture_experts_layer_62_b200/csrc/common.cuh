@@ -178,7 +178,7 @@ struct ScanArgs {
     const float* blockpsum;      // [NB][E] or null (then P, f, l_aux untouched)
     const float* blockextra;     // [NB][3] z-loss, entropy, gap sums, or null
     int32_t* indptr;             // [E+1]
-    void* stats;                 // moe_stats block
+    void* stats;                 // moe_stats block (its status word is the caller's to reset, before the router)
     // tile schedules (null pointers: skipped)
     int32_t* tiles13; int32_t* tiles2;   // [G+2]: cumulative tiles, then the split factor
     int tile_m, ntiles13, ntiles2, ntiles13_shared, ntiles2_shared, has_shared;

@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(const __grid_constan
             dropped += ce - kept_s[ee];
             maxc = max(maxc, ce);
         }
-        st->status = MOE_OK;
+        // (not the status: the call has reset it, and the router may have recorded a failure since)
         st->capacity = a.capacity;
         st->rows = tot_kept;
         st->dropped = dropped;
