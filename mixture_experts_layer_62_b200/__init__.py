@@ -663,8 +663,10 @@ class MoELayerInt8:
     each row (the given weights are not kept), activations quantised for each
     token on the way. A call launches, on the current stream, moe_route,
     moe_permute_int8, moe_expert_up_int8, moe_quantize_rows,
-    moe_expert_down_int8 and moe_combine (and for a shared expert the same
-    products with one expert over all tokens); it allocates nothing.
+    moe_expert_down_int8 and moe_combine_dropout without dropout (and for a
+    shared expert the same products with one expert over all tokens); it
+    allocates nothing. Every stage resets the status word that it is given, so
+    each has one of its own: read_stats() tells the first failure of a pass.
 
     p.train must be 0. With ``residual`` a call returns residual + layer(x).
     """
@@ -691,6 +693,10 @@ class MoELayerInt8:
         self.xq, self.xs, self.h = new((rows, d), _I8), new((rows,), _F32), new((rows, p.d_ff), dt)
         self.hq, self.hs, self.o = new((rows, p.d_ff), _I8), new((rows,), _F32), new((rows, d), dt)
         self.out, self.stats = new((T, d), dt), alloc_stats(p.E, dev)
+        # of the stages after the router: the permutation, and up, down (and the shared expert's up, down)
+        self.permutation_stats = alloc_stats(p.E, dev)
+        self.product_stats = torch.zeros((4 if p.d_ff_shared else 2, STATS_HEADER_BYTES), dtype=_U8, device=dev)
+        self._product_stats = self.product_stats.unbind()
         self.router_workspace = alloc_workspace(self.router, dev)
         self.workspace = alloc_int8_workspace(self.experts, dev)
         self.shared = None
@@ -701,35 +707,37 @@ class MoELayerInt8:
                                x=(new((T, d), _I8), new((T,), _F32)), h=new((T, f), dt),
                                hq=(new((T, f), _I8), new((T,), _F32)), s=new((T, d), dt),
                                indptr=torch.tensor([0, T], dtype=_I32, device=dev),
-                               workspace=alloc_int8_workspace(q, dev), stats=alloc_stats(1, dev))
+                               workspace=alloc_int8_workspace(q, dev))
 
     def __call__(self, x, out=None, residual=None, stream=None):
         out = self.out if out is None else out
         p, s = self.experts, None
         route(self.router, x, self.W_r, self.idx, self.gate, self.stats, self.router_workspace, bias=self.bias,
               stream=stream)
-        permute_int8(p, x, self.idx, self.pos, self.indptr, self.row_token, self.xq, self.xs, self.stats,
+        permute_int8(p, x, self.idx, self.pos, self.indptr, self.row_token, self.xq, self.xs, self.permutation_stats,
                      self.workspace, stream=stream)
         expert_up_int8(p, self.xq, self.xs, self.indptr, self.W1, self.w1s, self.W3, self.w3s, self.h,
-                       self.workspace, stats=self.stats, stream=stream)
+                       self.workspace, stats=self._product_stats[0], stream=stream)
         quantize_rows(self.h, self.hq, self.hs, used=self.used, stream=stream)
         expert_down_int8(p, self.hq, self.hs, self.indptr, self.W2, self.w2s, self.o, self.workspace,
-                         stats=self.stats, stream=stream)
+                         stats=self._product_stats[1], stream=stream)
         if self.shared is not None:
             g = self.shared
             s = g["s"]
             quantize_rows(x, *g["x"], stream=stream)
-            expert_up_int8(g["p"], *g["x"], g["indptr"], *g["W1"], *g["W3"], g["h"], g["workspace"], stats=g["stats"],
-                           stream=stream)
+            expert_up_int8(g["p"], *g["x"], g["indptr"], *g["W1"], *g["W3"], g["h"], g["workspace"],
+                           stats=self._product_stats[2], stream=stream)
             quantize_rows(g["h"], *g["hq"], stream=stream)
-            expert_down_int8(g["p"], *g["hq"], g["indptr"], *g["W2"], s, g["workspace"], stats=g["stats"],
+            expert_down_int8(g["p"], *g["hq"], g["indptr"], *g["W2"], s, g["workspace"], stats=self._product_stats[3],
                              stream=stream)
         combine_dropout(p, self.o, self.pos, self.gate, out, s=s, residual=residual, stream=stream)
         return out
 
     def read_stats(self) -> Stats:
-        """The layer's statistics; the status is the last product's that did not end with MOE_OK."""
+        """The layer's statistics; the status is that of the first stage of the
+        last pass that did not end with MOE_OK."""
         st = read_stats(self.stats, self.p.E)
-        if self.shared is not None and st.status == MOE_OK:
-            st.status = read_stats(self.shared["stats"], 1).status
+        later = [read_stats(self.permutation_stats, self.p.E).status,
+                 *self.product_stats.cpu().view(torch.int32)[:, 0].tolist()]
+        st.status = next((code for code in (st.status, *later) if code != MOE_OK), MOE_OK)
         return st
