@@ -34,13 +34,15 @@ def sweep(call, names):
 
     right, status, _ = timed()
     assert status == moe.MOE_OK
+    stopped = 0
     for limit in LIMITS:
         prev = moe.set_wait_limit(limit)
         try:
             for _ in range(3):
                 out, status, seconds = timed()
                 same = all(torch.equal(a, b) for a, b in zip(out, right))
-                assert status == moe.MOE_ERR_TIMEOUT or (status == moe.MOE_OK and same and limit > 1)
+                assert status == moe.MOE_ERR_TIMEOUT or (status == moe.MOE_OK and same)
+                stopped += status == moe.MOE_ERR_TIMEOUT
                 assert seconds < 1.0
         finally:
             moe.set_wait_limit(prev)
@@ -48,6 +50,7 @@ def sweep(call, names):
         assert status == moe.MOE_OK
         for name, a, b in zip(names, out, right):
             assert torch.equal(a, b), name
+    assert stopped > 0
 
 
 @pytest.mark.parametrize("T,d,dff,E,form", [

@@ -62,15 +62,17 @@ def test_a_wait_gives_up_anywhere(c, down):
     ref, bound = (a, R.plain_bound(a, torch.bfloat16)) if down else (R.swiglu(a, b), R.swiglu_bound(a, b, torch.bfloat16))
     right, status, _ = product(m, down)
     assert status == moe.MOE_OK and ((right.double() - ref).abs() <= bound).all()
+    stopped = 0
     for limit in LIMITS:
         prev = moe.set_wait_limit(limit)
         try:
             for _ in range(4):
                 out, status, seconds = product(m, down)
                 assert status == moe.MOE_ERR_TIMEOUT or (status == moe.MOE_OK and torch.equal(out, right))
-                assert status == moe.MOE_ERR_TIMEOUT or limit > 1
+                stopped += status == moe.MOE_ERR_TIMEOUT
                 assert seconds < 1.0
         finally:
             moe.set_wait_limit(prev)
         out, status, _ = product(m, down)
         assert status == moe.MOE_OK and torch.equal(out, right)
+    assert stopped > 0
