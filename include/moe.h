@@ -325,14 +325,16 @@ int moe_bias_update(const moe_problem* p, const void* stats, float gamma, float*
  * of 16 (bf16: 64, as everywhere), at most 131071 each (the sums stay below
  * 2^31), and d_ff_shared is 0: a shared expert is a second product with
  * E = k = 1 over moe_quantize_rows(x), indptr = {0, T}. Otherwise
- * MOE_ERR_UNSUPPORTED. Scales must be finite. Two calls that may overlap on
- * the GPU need a workspace each. */
+ * MOE_ERR_UNSUPPORTED. Scales are finite, or NaN: those make their row (or
+ * channel) of the result NaN. Two calls that may overlap on the GPU need a
+ * workspace each. */
 
 /* Rows in 8 bits, also for the weights (one call over the rows of a matrix):
  *   a_r = max_c |x[r,c]|, scale[r] = a_r / 127 (fp32),
  *   q[r,c] = the whole number nearest to 127 x[r,c] / a_r, ties to even,
  * decided exactly, so q depends on x alone. A row with a_r < 2^-100 gives
- * zeros and scale 0. x [rows, cols] of dtype MOE_DTYPE_*, q [rows, cols],
+ * zeros and scale 0, one that holds an infinity or a NaN zeros and scale NaN:
+ * all that is computed from it is NaN, and nothing else. x [rows, cols] of dtype MOE_DTYPE_*, q [rows, cols],
  * scale [rows]; cols % 16 == 0 (else MOE_ERR_UNSUPPORTED).
  * used: NULL, or one device integer: only the first min(rows, *used) rows
  * count, the others of q and scale stay as they are (pass &indptr[E] for the

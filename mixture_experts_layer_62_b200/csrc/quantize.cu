@@ -1,7 +1,9 @@
 // Rows in 8 bits: q_rc is the whole number nearest to 127 x_rc / a_r (ties to
 // even) with a_r = max_c |x_rc|, and scale_r = a_r / 127, so x ~ q scale with
 // an error of at most half a step a_r / 254. A row whose a_r is below 2^-100
-// (where 127 / a could overflow) is a row of zeros with scale 0.
+// (where 127 / a could overflow) is a row of zeros with scale 0. A row that
+// holds an infinity or a NaN is one of zeros with scale NaN, so that all that
+// is computed from it is NaN: the maxima pass a NaN on (max.NaN, as fast as max).
 //
 // One fused multiply-add rounds x inv, inv = 127 / a in fp32, to a whole
 // number; inv is off by 2^-24 relative, so near a border m + 1/2 the wrong
@@ -30,6 +32,7 @@ namespace moe {
 namespace {
 
 constexpr float kTinyRow = 7.888609052210118e-31f;   // 2^-100
+constexpr float kLargest = 3.402823466e+38f;
 constexpr float kMagic = 12582912.f;                 // 1.5 2^23: adding it rounds to a whole number, ties to even
 
 // ---- two-element fp32 arithmetic ----------------------------------------------
@@ -44,6 +47,11 @@ __device__ __forceinline__ void split2(uint64_t v, float& lo, float& hi) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 // 16 consecutive elements of a row, read past L1: each is read once, and a
@@ -62,9 +70,9 @@ template <> struct Vec16<__nv_bfloat16> {
     __device__ __forceinline__ float amax(float a) const {
         __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
 #pragma unroll
-        for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+        for (int i = 1; i < 8; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
         const float2 f = __bfloat1622float2(m);
-        return fmaxf(a, fmaxf(f.x, f.y));
+        return max_nan(a, max_nan(f.x, f.y));
     }
 };
 template <> struct Vec16<float> {
@@ -80,7 +88,7 @@ template <> struct Vec16<float> {
     __device__ __forceinline__ float hi(int i) const { return f[2 * i + 1]; }
     __device__ __forceinline__ float amax(float a) const {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(f[i]));
+        for (int i = 0; i < 16; ++i) a = max_nan(a, fabsf(f[i]));
         return a;
     }
 };
@@ -172,12 +180,16 @@ __device__ __forceinline__ float quantize_row(const Vec16<T> (&held)[kHold<T>], 
         a = w.amax(a);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    for (int o = 16; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
     if constexpr (TPR > 32) {
         if ((tid & 31) == 0) red[tid >> 5] = a;
         row_barrier<TPR>();
 #pragma unroll
-        for (int w = 0; w < TPR / 32; ++w) a = fmaxf(a, red[w]);
+        for (int w = 0; w < TPR / 32; ++w) a = max_nan(a, red[w]);
+    }
+    if (!(a <= kLargest)) {   // the threads of the row together
+        for (int v = tid; v < nv; v += TPR) put(v, make_uint4(0u, 0u, 0u, 0u));
+        return __int_as_float(0x7FC00000);
     }
     const bool live = a >= kTinyRow;
     const float inv = live ? inverse(a, &held[0]) : 0.f;
