@@ -11,6 +11,7 @@ tensors.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -422,6 +423,13 @@ def _on(stream, dev):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _stream_of(stream, device):
+    """Context in which memory is allocated for a call on this stream (an object, a handle, or None: the current one)."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device))
+
+
 def _rows(p: Problem) -> int:
     """permuted_rows without the call (p is checked by the library)."""
     return p.T * p.k + (p.E * (p.pad_rows - 1) if p.pad_rows > 0 else 0)
@@ -457,11 +465,11 @@ def int8_variant(p: Problem, down: bool = False) -> str:
 def quantize_rows(x, q=None, scale=None, used=None, stream=None):
     """Rows of x [..., cols] in 8 bits with a scale for each row (see
     moe_quantize_rows); used: a one-element int32 tensor, the rows to take.
-    Returns (q, scale), allocated here when not given."""
-    if q is None:
-        q = torch.empty(x.shape, dtype=_I8, device=x.device)
-    if scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=_F32, device=x.device)
+    Returns (q, scale), allocated here, on the stream of the call, when not given."""
+    if q is None or scale is None:
+        with _stream_of(stream, x.device):
+            q = torch.empty(x.shape, dtype=_I8, device=x.device) if q is None else q
+            scale = torch.empty(x.shape[:-1], dtype=_F32, device=x.device) if scale is None else scale
     rc = _bound().quantize_rows(x, q, scale, used, stream)
     if rc is None:
         dev = _device(x)
