@@ -133,14 +133,8 @@ def _load():
     lib.moe_combine_backward.restype = ctypes.c_int
     lib.moe_permute_backward.argtypes = [P] + [vp] * 4
     lib.moe_permute_backward.restype = ctypes.c_int
-    try:
-        from . import _binding
-    except ImportError as e:
-        raise ImportError("the package's binding is missing for this Python: build it with "
-                          "`python -m mixture_experts_layer_62_b200.build`") from e
-    _binding.attach(tuple(ctypes.cast(getattr(lib, "moe_" + n), vp).value for n in _BOUND))
     global _BINDING
-    _BINDING = _binding
+    _BINDING = _load_binding(lib)
     return lib
 
 
@@ -149,6 +143,29 @@ _BOUND = ("quantize_rows", "permute_int8", "expert_up_int8", "expert_down_int8",
           "permute_backward")
 _BINDING = None
 _LIB = None
+
+
+class _Unbound:
+    """In the place of a binding that is not there: takes no call, so that each
+    goes through the checks in this file and ctypes, the same call for some
+    microseconds more of the host."""
+
+    def __getattr__(self, name):
+        if name not in _BOUND:
+            raise AttributeError(name)
+        return lambda *args: None
+
+
+def _load_binding(lib):
+    """The compiled binding, where it is built for this Python and this torch."""
+    try:
+        from . import _binding
+    except ImportError:
+        return _Unbound()
+    if getattr(_binding, "torch_version", None) != torch.__version__:
+        return _Unbound()       # another torch's tensors may be laid out otherwise
+    _binding.attach(tuple(ctypes.cast(getattr(lib, "moe_" + n), ctypes.c_void_p).value for n in _BOUND))
+    return _binding
 
 
 def _bound():

@@ -101,7 +101,7 @@ def build(force=False, verbose=False, extra_flags=(), debug=False):
         cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
         incs = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(home, "include"), os.path.join(cuda, "include")]
         run([os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
-             *[f for i in incs for f in ("-I", i)], src, "-o", BINDING_PATH, "-L", os.path.join(home, "lib"),
+             f'-DMOE_TORCH_VERSION="{torch.__version__}"', *[f for i in incs for f in ("-I", i)], src, "-o", BINDING_PATH, "-L", os.path.join(home, "lib"),
              "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
     return lib_path
 

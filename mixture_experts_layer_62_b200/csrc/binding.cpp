@@ -287,5 +287,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 PyMODINIT_FUNC PyInit__binding(void) {
     s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-    return PyModule_Create(&module);
+    PyObject* m = PyModule_Create(&module);
+    // the torch whose tensors it reads: the package loads it beside no other
+    if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", MOE_TORCH_VERSION) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
 }
