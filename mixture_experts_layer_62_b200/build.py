@@ -11,7 +11,7 @@ MOE_DEBUG into _build_debug/ and libmoe_debug.so: the library with the
 device-side bounds checks that record MOE_ERR_BOUNDS (include/moe.h).
 Either way csrc/binding.cpp, the package's own calls of some of the library's
 functions, is compiled for the running Python and torch with the host's C++
-compiler.
+compiler, and again when another torch is installed.
 """
 
 from __future__ import annotations
@@ -32,6 +32,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libmoe.so")
 DEBUG_BUILD_DIR = os.path.join(ROOT, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libmoe_debug.so")
+BINDING_STAMP = os.path.join(BUILD_DIR, "binding.torch")   # the torch that the binding was compiled against
 BINDING_PATH = os.path.join(PKG_DIR, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 SOURCES = ["api.cu", "route.cu", "permute.cu", "combine.cu", "gemm_simt.cu", "gemm_sm100.cu",
@@ -60,6 +61,21 @@ def _stale(target, inputs):
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(i) > t for i in inputs)
+
+
+def _torch_stamp():
+    import torch
+    return f"{torch.__version__} abi{int(torch.compiled_with_cxx11_abi())}"
+
+
+def _binding_stale():
+    """The binding is missing, older than what it is made of, or another torch's."""
+    if _stale(BINDING_PATH, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "moe.h")]):
+        return True
+    if not os.path.exists(BINDING_STAMP):
+        return True
+    with open(BINDING_STAMP) as f:
+        return f.read() != _torch_stamp()
 
 
 def build(force=False, verbose=False, extra_flags=(), debug=False):
@@ -94,15 +110,18 @@ def build(force=False, verbose=False, extra_flags=(), debug=False):
     if force or jobs or _stale(lib_path, objs):
         cmd = [nvcc, *ARCH_FLAGS, "-shared", "-o", lib_path, *objs]
         run(cmd)
-    src = os.path.join(CSRC, "binding.cpp")
-    if force or _stale(BINDING_PATH, [src, os.path.join(INCLUDE, "moe.h")]):
+    if force or _binding_stale():
         import torch
         home = os.path.dirname(torch.__file__)
         cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
         incs = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(home, "include"), os.path.join(cuda, "include")]
         run([os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
-             f'-DMOE_TORCH_VERSION="{torch.__version__}"', *[f for i in incs for f in ("-I", i)], src, "-o", BINDING_PATH, "-L", os.path.join(home, "lib"),
-             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+             f'-DMOE_TORCH_VERSION="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+             *[f for i in incs for f in ("-I", i)], os.path.join(CSRC, "binding.cpp"), "-o", BINDING_PATH,
+             "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+        os.makedirs(BUILD_DIR, exist_ok=True)
+        with open(BINDING_STAMP, "w") as f:
+            f.write(_torch_stamp())
     return lib_path
 
 

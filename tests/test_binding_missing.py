@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import mixture_experts_layer_62_b200 as moe
+from mixture_experts_layer_62_b200 import build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HIDE = {
@@ -43,6 +44,19 @@ def test_the_binding_is_this_torchs():
     assert moe._bound().torch_version == torch.__version__
     with pytest.raises(AttributeError):
         moe._Unbound().no_such_call
+
+
+def test_the_binding_is_compiled_again_for_another_torch(tmp_path, monkeypatch):
+    module, stamp = tmp_path / "binding.so", tmp_path / "binding.torch"
+    monkeypatch.setattr(build, "BINDING_PATH", str(module))
+    monkeypatch.setattr(build, "BINDING_STAMP", str(stamp))
+    assert build._binding_stale()               # nothing there
+    module.write_bytes(b"")
+    assert build._binding_stale()               # compiled against nobody knows what
+    stamp.write_text(build._torch_stamp())
+    assert not build._binding_stale()
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    assert build._binding_stale()
 
 
 @pytest.mark.gpu
