@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -682,6 +683,19 @@ class MoELayer:
         return read_stats(self.stats, self.p.E)
 
 
+def _aligned_bytes(shape, dtype) -> int:
+    """Bytes of a tensor, rounded up to the alignment of a workspace."""
+    return -(-math.prod(shape) * dtype.itemsize // 256) * 256
+
+
+def _split(memory, parts):
+    """Tensors of the (shape, dtype) of parts, one behind another in memory (uint8)."""
+    at = 0
+    for shape, dtype in parts:
+        yield memory[at:at + math.prod(shape) * dtype.itemsize].view(dtype).view(shape)
+        at += _aligned_bytes(shape, dtype)
+
+
 class MoELayerInt8:
     """MoELayer with the experts in 8 bits: the same arguments, the router in
     the problem's type, every expert weight quantised here with a scale for
@@ -705,7 +719,6 @@ class MoELayerInt8:
         self.experts = Problem.from_buffer_copy(p)
         self.experts.d_ff_shared = 0
         rows = permuted_rows(self.experts)
-        # the router's workspace holds buffers of the whole layer: a problem of the smallest hidden width
         self.router = Problem.from_buffer_copy(self.experts)
         self.router.d_ff = 64
         new = lambda shape, t: torch.empty(shape, dtype=t, device=dev)  # noqa: E731
@@ -715,14 +728,19 @@ class MoELayerInt8:
         self.idx, self.gate, self.pos = new((T, p.k), _I32), new((T, p.k), _F32), new((T, p.k), _I32)
         self.indptr, self.row_token = new((p.E + 1,), _I32), new((rows,), _I32)
         self.used = self.indptr[p.E:]
-        self.xq, self.xs, self.h = new((rows, d), _I8), new((rows,), _F32), new((rows, p.d_ff), dt)
-        self.hq, self.hs, self.o = new((rows, p.d_ff), _I8), new((rows,), _F32), new((rows, d), dt)
+        # The router's workspace has room for buffers of a whole layer. It is done with
+        # before the first of the rows behind it is written, so it lies over them.
+        rest = (((rows, d), _I8), ((rows,), _F32), ((rows, p.d_ff), dt), ((rows, p.d_ff), _I8), ((rows,), _F32),
+                ((rows, d), dt))
+        need = workspace_size(self.router)
+        memory = new((max(need, sum(_aligned_bytes(*part) for part in rest)),), _U8)
+        self.router_workspace = memory[:need]
+        self.xq, self.xs, self.h, self.hq, self.hs, self.o = _split(memory, rest)
         self.out, self.stats = new((T, d), dt), alloc_stats(p.E, dev)
         # of the stages after the router: the permutation, and up, down (and the shared expert's up, down)
         self.permutation_stats = alloc_stats(p.E, dev)
         self.product_stats = torch.zeros((4 if p.d_ff_shared else 2, STATS_HEADER_BYTES), dtype=_U8, device=dev)
         self._product_stats = self.product_stats.unbind()
-        self.router_workspace = alloc_workspace(self.router, dev)
         self.workspace = alloc_int8_workspace(self.experts, dev)
         self.shared = None
         if p.d_ff_shared:
