@@ -412,7 +412,7 @@ def permute_noalloc(p: Problem, x, idx, pos, indptr, row_token, xp, stats, strea
 
 def _device(t) -> int:
     """The current device, which the tensors of a call have to be on."""
-    if not t.is_cuda:
+    if t is None or not t.is_cuda:
         raise ValueError("tensors passed to the MoE library must be CUDA tensors")
     return torch._C._cuda_getDevice()
 
@@ -421,6 +421,8 @@ def _arg(t, dtype, numel, name, dev):
     """Address of a tensor of the current device with at least numel elements
     of dtype (another type, or fewer, would be read as something else or past
     the end)."""
+    if t is None:
+        raise ValueError(f"{name}: expected {dtype} with at least {numel} elements, got None")
     if t.dtype is not dtype or t.numel() < numel:
         raise ValueError(f"{name}: expected {dtype} with at least {numel} elements, got {t.dtype} with {t.numel()}")
     if t.get_device() != dev:
