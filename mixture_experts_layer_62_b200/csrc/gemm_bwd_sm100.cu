@@ -437,7 +437,7 @@ tc_bwd_gemm(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUte
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) {   // a wait gave up: what was started lands
+    if (__builtin_expect(*reinterpret_cast<volatile int*>(&ctl->abort_flag), 0)) {   // a wait gave up: what was started lands
         if (threadIdx.x == 0) {
             for (uint32_t j = ctl->loaded > STAGES ? ctl->loaded - STAGES : 0; j < ctl->loaded; ++j)
                 wait_d(&ctl->full[j % STAGES], (j / STAGES) & 1u, p);

@@ -91,6 +91,7 @@ struct Ctl {
     uint32_t tmem_base;
     int abort_flag;
     uint32_t loaded;          // K blocks that the CTA has requested, written as its loads end
+    uint32_t bytes[STAGES];   // pair: what it has requested of the last block in each stage
     int cum[MOE_MAX_E + 1];   // tiles before group g
     int row0[MOE_MAX_E + 1];  // first row of group g
     int most;                 // rows of the tallest tile
@@ -203,6 +204,7 @@ __device__ __forceinline__ void drain_i8(uint64_t* bar, uint32_t parity, const K
 // The last requests of every stage: block j of `n` completes phase (j / STAGES) % 2 of full[j % STAGES].
 template <int STAGES>
 __device__ __forceinline__ void drain_loads(Ctl<STAGES>* ctl, uint32_t n, const KP& p) {
+#pragma unroll 1
     for (uint32_t j = n > STAGES ? n - STAGES : 0; j < n; ++j) drain_i8(&ctl->full[j % STAGES], (j / STAGES) & 1u, p);
 }
 
@@ -558,11 +560,6 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int num_kb = (p.K + BKB - 1) / BKB;
     constexpr int SET = SWIGLU ? 128 : 256;   // channels of one of a tile's two sets
     auto sets_of = [&](const Item& it) { return it.t.n_blk * 2 * SET + SET < p.N ? 2 : 1; };
-    auto boxes_of = [&](const Item& it) { return it.shrt ? ((it.n + 31) / 32 * 16 + 31) / 32 : 0; };
-    // bytes of a K block that each of the two CTAs loads
-    auto tx_of = [&](const Item& it) -> uint32_t {
-        return (it.shrt ? boxes_of(it) * 32 * BKB : A_BYTES) + sets_of(it) * BH_BYTES;
-    };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -577,17 +574,18 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 // this rank's rows of A: 128 in one box, or of a short tile half of its N columns in boxes of 32
                 const int half_n = (it.n + 31) / 32 * 16;
                 const int arow = static_cast<int>(it.row0) + rank * (it.shrt ? half_n : BM);
-                const int boxes = boxes_of(it);
+                const int boxes = it.shrt ? (half_n + 31) / 32 : 0;
                 // its two 64-row boxes of weights of each set
                 const int b0 = it.t.g * p.N + it.t.n_blk * 2 * SET + (SWIGLU ? (it.shrt ? rank * 64 : 0) : rank * 128);
                 const int b1 = SWIGLU && it.shrt ? b0 : b0 + 64;
                 const CUtensorMap* m0 = SWIGLU && !it.shrt && rank ? &tmB1 : &tmB0;
                 const CUtensorMap* m1 = SWIGLU && it.shrt ? &tmB1 : m0;
-                const uint32_t bytes = tx_of(it);
+                const uint32_t bytes = (it.shrt ? boxes * 32 * BKB : A_BYTES) + sets * BH_BYTES;
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (!wait_i8(&ctl->empty[s], ph ^ 1u, ctl, p, peer_abort)) { aborted = true; break; }
                     const uint32_t sa = smem_u32(smem + s * P_STAGE_BYTES);
                     if (leader) mbar_arrive_expect_tx(&ctl->full[s], 2 * bytes);
+                    ctl->bytes[s] = bytes;
                     if (it.shrt) {
                         for (int q = 0; q < boxes; ++q)
                             tma_load_2d_pair(sa + q * 32 * BKB, &tmA32, full_of(s), kb * BKB, arow + 32 * q);
@@ -783,23 +781,18 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     // A wait gave up (both CTAs carry the flag): the leader's barriers count both CTAs' copies, so it
     // waits for all of them. Where one CTA has requested more blocks than the other, the bytes that will
     // not come are taken off the leader's phase, or the phase is armed for the other CTA's alone.
-    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) {
-        if (leader && threadIdx.x == 0) {
-            const uint32_t n0 = ctl->loaded, n1 = ld_shared_remote_u32(mapa_shared(smem_u32(&ctl->loaded), 1u));
-            uint32_t j = 0;   // blocks up to the end of the item
-            const uint32_t lo = min(n0, n1), hi = max(n0, n1);
-            for (int u = cluster; u < work.items && j < hi; u += nclusters) {
-                const Item it = item_at(ctl, p, work, u);
-                if (it.n == 0) continue;
-                const uint32_t from = max(j, lo), to = min(j + num_kb, hi);
-                for (uint32_t b = from; b < to; ++b) {
-                    if (n0 > n1) mbar_complete_tx(&ctl->full[b % P_STAGES], tx_of(it));
-                    else mbar_arrive_expect_tx(&ctl->full[b % P_STAGES], tx_of(it));
-                }
-                j += num_kb;
+    if (__builtin_expect(*reinterpret_cast<volatile int*>(&ctl->abort_flag), 0)) {
+        if (cluster_ctarank() == 0 && threadIdx.x == 0) {
+            auto other = [](const uint32_t* v) { return ld_shared_remote_u32(mapa_shared(smem_u32(v), 1u)); };
+            const uint32_t n0 = ctl->loaded, n1 = other(&ctl->loaded);
+            const uint32_t hi = max(n0, n1);
+#pragma unroll 1
+            for (uint32_t j = min(n0, n1); j < hi; ++j) {
+                if (n0 > n1) mbar_complete_tx(&ctl->full[j % P_STAGES], ctl->bytes[j % P_STAGES]);
+                else mbar_arrive_expect_tx(&ctl->full[j % P_STAGES], other(&ctl->bytes[j % P_STAGES]));
             }
             drain_loads(ctl, hi, p);
-        } else if (leader && threadIdx.x == 32) {
+        } else if (cluster_ctarank() == 0 && threadIdx.x == 32) {
             tc_commit_pair(&ctl->drain);
             drain_i8(&ctl->drain, 0, p);
         }
@@ -808,9 +801,9 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         cluster_sync_all();
         tc_fence_after();
     }
-    if (warp == 1) {
+    if (threadIdx.x >> 5 == 1) {
         __syncwarp();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(ctl->tmem_base), "r"(TMEM_COLS)
                      : "memory");
     }
 }
@@ -1113,7 +1106,7 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) {   // a wait gave up
+    if (__builtin_expect(*reinterpret_cast<volatile int*>(&ctl->abort_flag), 0)) {   // a wait gave up
         if (threadIdx.x == 0) {
             drain_loads(ctl, ctl->loaded, p);
         } else if (threadIdx.x == 32) {
@@ -1125,9 +1118,9 @@ i8_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         __syncthreads();
         tc_fence_after();
     }
-    if (warp == 1) {
+    if (threadIdx.x >> 5 == 1) {
         __syncwarp();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(ctl->tmem_base), "r"(TMEM_COLS)
                      : "memory");
     }
 }

@@ -715,7 +715,7 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) {   // a wait gave up: what was started lands
+    if (__builtin_expect(*reinterpret_cast<volatile int*>(&ctl->abort_flag), 0)) {   // a wait gave up: what was started lands
         if (threadIdx.x == 0) {
             for (uint32_t j = ctl->loaded > STAGES ? ctl->loaded - STAGES : 0; j < ctl->loaded; ++j)
                 wait_drain(&ctl->full[j % STAGES], (j / STAGES) & 1u, p);
@@ -1100,7 +1100,7 @@ tc_pair_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ C
     // leader's barriers count both CTAs' bytes; where one has requested more
     // blocks than the other, the bytes that will not come are taken off the
     // leader's phase, or the phase is armed for the other CTA's alone.
-    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) {
+    if (__builtin_expect(*reinterpret_cast<volatile int*>(&ctl->abort_flag), 0)) {
         if (leader && threadIdx.x == 0) {
             const uint32_t n0 = ctl->loaded, n1 = ld_shared_remote_u32(mapa_shared(smem_u32(&ctl->loaded), 1u));
             const uint32_t hi = max(n0, n1);
