@@ -320,7 +320,7 @@ int moe_bias_update(const moe_problem* p, const void* stats, float gamma, float*
  * signed 8-bit activations and weights, a scale for each token and for each
  * weight row (channel), and exact 32-bit integer sums. A forward in 8 bits is
  *   moe_route, moe_permute_int8, moe_expert_up_int8, moe_quantize_rows (the
- *   hidden rows), moe_expert_down_int8, moe_combine.
+ *   hidden rows), moe_expert_down_int8, moe_combine or moe_combine_dropout.
  * p->dtype (bf16 or f32) is the type of x, h and o. d and d_ff are multiples
  * of 16 (bf16: 64, as everywhere), at most 131071 each (the sums stay below
  * 2^31), and d_ff_shared is 0: a shared expert is a second product with
@@ -349,9 +349,10 @@ size_t moe_int8_workspace_size(const moe_problem* p);
 
 /* Which form a product of p takes (down = 0: up, else down):
  * MOE_INT8_PAIR (CTA pairs, tiles of 256 rows x 512 weight rows) where the
- * experts average at least 256 rows and the tiles fill the GPU,
- * MOE_INT8_SINGLE (single CTAs, the weights as the M operand, the last tiles
- * cut along K) otherwise. The sums are exact and the scales applied alike: the
+ * experts average enough rows for the product's K (the longer it is, the
+ * fewer), the channels fill most of their tiles and there are tiles for most
+ * of the GPU; MOE_INT8_SINGLE (single CTAs, the weights as the M operand, the
+ * last tiles cut along K) otherwise. The sums are exact and the scales applied alike: the
  * results are the same bits. A negative MOE_ERR_* code if p is not one they
  * take. Host only. */
 #define MOE_INT8_SINGLE 0
@@ -376,7 +377,8 @@ int moe_permute_int8(const moe_problem* p, const void* x, const int32_t* idx,
  * stay. indptr as in moe_experts; a group whose offsets do not fit the rows is
  * left out (and recorded as MOE_ERR_BOUNDS by the debug build). stats (may be
  * NULL): only the status word is written (MOE_OK, or MOE_ERR_TIMEOUT if a
- * bounded wait gave up). */
+ * bounded wait gave up). As in every call, it starts from MOE_OK: calls that
+ * are looked at together later need a statistics block each. */
 int moe_expert_up_int8(const moe_problem* p, const int8_t* xq, const float* xs, const int32_t* indptr,
                        const int8_t* W1, const float* w1s, const int8_t* W3, const float* w3s,
                        void* h, void* stats, void* workspace, size_t workspace_bytes, void* stream);

@@ -1,10 +1,10 @@
 """B200 (sm_100a) forward pass of one sparse Mixture-of-Experts layer.
 
 A thin ctypes binding over the C ABI of ``libmoe.so`` (declared in
-``include/moe.h``; some calls go through a compiled module, ``_bound``). The
-functions here only marshal arguments: every step of the layer runs in the
-library's CUDA kernels. PyTorch provides device memory
-and the current stream. There is no CPU fallback: importing this package
+``include/moe.h``; some calls go through a compiled module, ``_bound``, where
+it is built for this Python and this torch). The functions here only marshal
+arguments: every step of the layer runs in the library's CUDA kernels. PyTorch
+provides device memory and the current stream. There is no CPU fallback: importing this package
 raises if the library has not been built, and every call requires CUDA
 tensors.
 """

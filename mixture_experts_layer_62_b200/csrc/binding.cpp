@@ -3,7 +3,8 @@
 // at every tensor once (type, elements, device, contiguity, address) and makes
 // the library's call. It returns the call's code, or None, with nothing done,
 // when an argument is not as it has to be: the caller then goes through its
-// own checks, which say what is wrong. Microseconds of the host for a pass of 9
+// own checks, which say what is wrong, and which make the call by ctypes where
+// this module is missing or another torch's. Microseconds of the host for a pass of 9
 // tokens, d = d_ff = 64, against ctypes: quantisation and down product 16.0 ->
 // 9.1, permutation and up product 18.4 -> 9.6, the way back and its gradient
 // 13.2 -> 5.4.

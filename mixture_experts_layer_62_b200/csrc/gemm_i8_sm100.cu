@@ -245,7 +245,9 @@ constexpr float kNegLog2e = -1.4426950408889634f;
 // reciprocal (a few 2^-23 off, where the type rounds to 2^-8); fp32 results:
 // the accurate exponential, and the reciprocal of one unit in the last place
 // with subnormal results kept (a divide in its place: 156 us where this takes
-// 100; 3000 rows, K = 64, 11328 channels). exp(-a) overflowing gives a 0, as it should.
+// 100; 3000 rows, K = 64, 11328 channels). Against 64 bits the results of eight
+// shapes, K = 64 to 4096, are 1.41 to 1.49 steps of 2^-24 off (rms); with the
+// reciprocal corrected by a Newton step 1.39 to 1.48, and up to 6 % later. exp(-a) overflowing gives a 0, as it should.
 __device__ __forceinline__ float rcp_full(float x) {
     float r;
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));

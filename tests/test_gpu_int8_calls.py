@@ -136,3 +136,22 @@ def test_two_host_threads():
     for t in threads:
         t.join()
     assert not wrong and all(layer.read_stats().status == moe.MOE_OK for layer, _, _, _ in layers)
+
+
+def test_no_tokens():
+    # (the tensors have a row each: pointers are checked before anything else)
+    E, d, dff = 4, 64, 128
+    p = moe.problem(0, d, dff, E, 2)
+    one = lambda *s, t=torch.int32: torch.full(s, 3, dtype=t, device=DEV)  # noqa: E731
+    x, h, o = (one(1, n, t=torch.bfloat16) for n in (d, dff, d))
+    indptr, st, work = one(E + 1), moe.alloc_stats(E, DEV), moe.alloc_int8_workspace(p, DEV)
+    st.fill_(255)
+    q, s = one(1, d, t=torch.int8), one(1, t=torch.float32)
+    moe.permute_int8(p, x, one(1, 2), one(1, 2), indptr, one(2), q, s, st, work)
+    W, V, a, b = one(E, dff, d, t=torch.int8), one(E, d, dff, t=torch.int8), torch.ones((E, dff), device=DEV), torch.ones((E, d), device=DEV)
+    moe.expert_up_int8(p, q, s, indptr, W, a, W, a, h, work)
+    moe.expert_down_int8(p, one(1, dff, t=torch.int8), s, indptr, V, b, o, work)
+    moe.quantize_rows(h[:0], one(1, dff, t=torch.int8), s)
+    assert (indptr == 0).all() and (h == 3).all() and (o == 3).all() and (q == 3).all() and (s == 3).all()
+    got = moe.read_stats(st, E)
+    assert got.status == moe.MOE_OK and got.rows == got.dropped == got.max_count == 0 and not any(got.counts)
