@@ -730,14 +730,14 @@ class MoELayerInt8:
         self.idx, self.gate, self.pos = new((T, p.k), _I32), new((T, p.k), _F32), new((T, p.k), _I32)
         self.indptr, self.row_token = new((p.E + 1,), _I32), new((rows,), _I32)
         self.used = self.indptr[p.E:]
-        # The router's workspace has room for buffers of a whole layer. It is done with
-        # before the first of the rows behind it is written, so it lies over them.
+        # The router's workspace has room for buffers of a whole layer, of which it uses
+        # what stands before the first of them; the rows behind the router lie over the others.
         rest = (((rows, d), _I8), ((rows,), _F32), ((rows, p.d_ff), dt), ((rows, p.d_ff), _I8), ((rows,), _F32),
                 ((rows, d), dt))
-        need = workspace_size(self.router)
-        memory = new((max(need, sum(_aligned_bytes(*part) for part in rest)),), _U8)
+        need, at = workspace_size(self.router), workspace_layout(self.router)["xp"]
+        memory = new((max(need, at + sum(_aligned_bytes(*part) for part in rest)),), _U8)
         self.router_workspace = memory[:need]
-        self.xq, self.xs, self.h, self.hq, self.hs, self.o = _split(memory, rest)
+        self.xq, self.xs, self.h, self.hq, self.hs, self.o = _split(memory[at:], rest)
         self.out, self.stats = new((T, d), dt), alloc_stats(p.E, dev)
         # of the stages after the router: the permutation, and up, down (and the shared expert's up, down)
         self.permutation_stats = alloc_stats(p.E, dev)

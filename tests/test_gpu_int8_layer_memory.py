@@ -31,7 +31,8 @@ def test_memory_of_the_layer(T, d, dff, E, k, dtype, pad):
     weights = 3 * E * dff * d + 4 * E * (2 * dff + d)
     behind_router = rows * (d + 4 + dff * dt.itemsize + dff + 4 + d * dt.itemsize)
     tokens = T * (d * dt.itemsize + 12 * k) + 4 * rows
-    need = weights + max(behind_router, layer.router_workspace.nbytes) + tokens + layer.workspace.nbytes
+    router = moe.workspace_layout(layer.router)["xp"]       # what it uses
+    need = weights + max(router + behind_router, layer.router_workspace.nbytes) + tokens + layer.workspace.nbytes
     assert taken <= need + (1 << 20)
     y = layer(x).clone()
 
@@ -53,3 +54,7 @@ def test_memory_of_the_layer(T, d, dff, E, k, dtype, pad):
         assert torch.equal(a, b)
     for _ in range(3):
         assert torch.equal(layer(x), y)
+    # what the router left in its workspace is still there behind the pass
+    logits = torch.zeros((T, E), device=DEV)
+    moe.route(p, x, w["W_r"], idx, gate, st, moe.alloc_workspace(p, DEV), logits=logits)
+    assert torch.equal(moe.workspace_view(layer.router_workspace, layer.router, "logits"), logits)
